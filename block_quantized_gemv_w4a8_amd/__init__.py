@@ -38,6 +38,11 @@ QGEMV_VARIANT_MFMA_STAGED, QGEMV_VARIANT_MFMA_STREAM, QGEMV_VARIANT_MFMA_RESIDEN
 QGEMV_K_MAX = 32768
 QGEMV_MULTI_MAX = 8
 QGEMV_M_MAX = 64
+QGEMV_TYPE_F32, QGEMV_TYPE_F16, QGEMV_TYPE_BF16 = 0, 1, 2
+QGEMV_ROPE_HALVES, QGEMV_ROPE_PAIRS = 0, 1
+QGEMV_HEAD_DIM_MAX = 256
+QGEMV_W8A8_K_MAX = 131071
+QGEMV_WS_BYTES = 64 << 20
 
 # Every extern "C" symbol that include/qgemv.h declares.
 EXPORTS = [
@@ -49,6 +54,8 @@ EXPORTS = [
     "qgemv_silu_mul_quantize", "qgemv_q4_k_swiglu_quantize",
     "qgemv_quantize_gemv", "qgemv_quantize_q4_k_swiglu", "qgemv_multi", "qgemv_quantize_multi",
     "qgemv_block_dots", "qgemv_block_dots_staged", "qgemm_small_m_block_dots",
+    "qgemv_rope_append", "qgemv_paged_attn", "qgemv_quantize_rows", "qgemm_w8a8",
+    "qgemm_quantize_w8a8",
 ]
 
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -304,6 +311,83 @@ def qgemm_small_m_block_dots(fmt, w, N, K, M, q, d, s, y, variant, dots, stream=
     return _check(_lib.qgemm_small_m_block_dots(fmt, _ptr(w), N, K, M, _ptr(q), _ptr(d), _ptr(s),
                                                 _ptr(y), variant, _ptr(dots), _stream(stream)),
                   "qgemm_small_m_block_dots")
+
+
+class KvCache(ctypes.Structure):
+    """qgemv_kv_cache of the header; kv_cache() fills one from torch tensors."""
+    _fields_ = [("k", _P), ("v", _P), ("page_stride", _I64), ("token_stride", _I64),
+                ("head_stride", _I64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+_KV = ctypes.POINTER(KvCache)
+_F = ctypes.c_float
+_lib.qgemv_rope_append.restype = _I
+_lib.qgemv_rope_append.argtypes = [_KV, _I64, _I, _P, _I64, _I, _P, _I64, _P, _I64, _P, _P, _P, _I,
+                                   _I, _P, _I64, _P]
+_lib.qgemv_paged_attn.restype = _I
+_lib.qgemv_paged_attn.argtypes = [_KV, _P, _I64, _I64, _I, _P, _P, _I, _I, _I64, _P, _I64, _F, _I,
+                                  _I, _P, _I, _I64, _P, _P, _I64, _P]
+_lib.qgemv_quantize_rows.restype = _I
+_lib.qgemv_quantize_rows.argtypes = [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P]
+_lib.qgemm_w8a8.restype = _I
+_lib.qgemm_w8a8.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I, _I64, _P,
+                            _I64, _P]
+_lib.qgemm_quantize_w8a8.restype = _I
+_lib.qgemm_quantize_w8a8.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _I64, _P,
+                                     _P, _P, _I, _I64, _P, _I64, _P]
+
+
+def kv_cache(k, v) -> KvCache:
+    """Descriptor of the pools k and v, torch tensors [pages, page_size, heads, head_dim] of
+    one type and one set of strides (a heads-major pool is passed as its transposed view).
+    It holds addresses only: the pools must outlive it."""
+    import torch
+    types = {torch.float16: QGEMV_TYPE_F16, torch.bfloat16: QGEMV_TYPE_BF16}
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in types:
+        raise ValueError("k and v must be 4-D tensors of one shape, both fp16 or both bf16")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v must have the same strides, with head_dim contiguous")
+    return KvCache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0],
+                   k.shape[1], k.shape[2], k.shape[3], types[k.dtype])
+
+
+def qgemv_rope_append(cache, T, in_type, q, ldq, q_heads, k, ldk, v, ldv, pos, slots, inv_freq,
+                      rot_dim, style, q_out, ldqo, stream=None):
+    return _check(_lib.qgemv_rope_append(cache, T, in_type, _ptr(q), ldq, q_heads, _ptr(k), ldk,
+                                         _ptr(v), ldv, _ptr(pos), _ptr(slots), _ptr(inv_freq),
+                                         rot_dim, style, _ptr(q_out), ldqo, _stream(stream)),
+                  "qgemv_rope_append")
+
+
+def qgemv_paged_attn(cache, q, T, ldq, q_heads, q_start, kv_len, B, max_q, max_kv, table, ldt,
+                     scale, window, sinks, out, out_type, ldo, lse=None, ws=None, ws_bytes=0,
+                     stream=None):
+    return _check(_lib.qgemv_paged_attn(cache, _ptr(q), T, ldq, q_heads, _ptr(q_start),
+                                        _ptr(kv_len), B, max_q, max_kv, _ptr(table), ldt, scale,
+                                        window, sinks, _ptr(out), out_type, ldo, _ptr(lse),
+                                        _ptr(ws), ws_bytes, _stream(stream)), "qgemv_paged_attn")
+
+
+def qgemv_quantize_rows(x, x_type, M, K, ldx, q, ldq, sx, stream=None):
+    return _check(_lib.qgemv_quantize_rows(_ptr(x), x_type, M, K, ldx, _ptr(q), ldq, _ptr(sx),
+                                           _stream(stream)), "qgemv_quantize_rows")
+
+
+def qgemm_w8a8(w, ldw, sw, N, K, M, q, ldq, sx, bias, y, y_type, ldy, ws=None, ws_bytes=0,
+               stream=None):
+    return _check(_lib.qgemm_w8a8(_ptr(w), ldw, _ptr(sw), N, K, M, _ptr(q), ldq, _ptr(sx),
+                                  _ptr(bias), _ptr(y), y_type, ldy, _ptr(ws), ws_bytes,
+                                  _stream(stream)), "qgemm_w8a8")
+
+
+def qgemm_quantize_w8a8(w, ldw, sw, N, K, M, x, x_type, ldx, q, ldq, sx, bias, y, y_type, ldy,
+                        ws=None, ws_bytes=0, stream=None):
+    return _check(_lib.qgemm_quantize_w8a8(_ptr(w), ldw, _ptr(sw), N, K, M, _ptr(x), x_type, ldx,
+                                           _ptr(q), ldq, _ptr(sx), _ptr(bias), _ptr(y), y_type,
+                                           ldy, _ptr(ws), ws_bytes, _stream(stream)),
+                  "qgemm_quantize_w8a8")
 
 
 GEMV = {"q4_0": qgemv_q4_0, "q4_k": qgemv_q4_k, "q6_k": qgemv_q6_k, "q8_0": qgemv_q8_0,

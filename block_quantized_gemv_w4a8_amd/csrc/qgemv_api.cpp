@@ -17,6 +17,7 @@
 
 #include "qgemv.h"
 #include "qgemv_launch.h"
+#include "qgemv_layer.h"
 
 static_assert(QGEMV_MULTI_MAX == qgemv::kMultiMax, "one limit for the multi-matrix entries");
 
@@ -552,3 +553,5 @@ qgemv_status qgemv_block_dots_staged(int fmt, const void* w, int64_t N, int64_t 
 }
 
 }  // extern "C"
+
+#include "qgemv_layer_api.h"

@@ -1,5 +1,6 @@
 /*
- * qgemv.h -- C ABI of libqgemv: W4A8 block-quantized GEMV for AMD MI355X (gfx950).
+ * qgemv.h -- C ABI of libqgemv: W4A8 block-quantized GEMV for AMD MI355X (gfx950),
+ * and the attention block and int8 products of the layer around it (last part).
  *
  * The operation ("Backends and hardware", llamay docs, section "CPU"): the
  * activation is quantised to int8 once per matmul, in blocks of 32 with an
@@ -383,6 +384,128 @@ qgemv_status qgemv_block_dots_staged(int fmt, const void* w, int64_t N, int64_t 
                                      int64_t row0, int64_t nrows, const int8_t* q,
                                      const uint16_t* d, const int32_t* s, int wk,
                                      int32_t* dots, qgemv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the weight products of a decoder layer: the rotation of new q and k
+ * rows and their place in a paged cache, the attention over that cache, and
+ * products of int8 codes with one scale per token and per output channel for
+ * any number of tokens.  The conventions above hold here too; in addition,
+ * arrays of lengths, starts, positions, slots and page numbers live on the
+ * device, so their contents cannot be refused by a gate: every kernel bounds
+ * them itself, as stated at each entry, and never reads or writes outside the
+ * buffers it was given.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the entries below. */
+enum { QGEMV_TYPE_F32 = 0, QGEMV_TYPE_F16 = 1, QGEMV_TYPE_BF16 = 2 };
+/* Which values of a head turn together: i and i + rot/2, or 2i and 2i + 1. */
+enum { QGEMV_ROPE_HALVES = 0, QGEMV_ROPE_PAIRS = 1 };
+
+/* Largest head_dim of a cache, and largest K of a w8a8 product (the int32 sum
+ * of K products of two codes, each at most 128 in size, cannot overflow). */
+#define QGEMV_HEAD_DIM_MAX 256
+#define QGEMV_W8A8_K_MAX 131071
+/* A workspace that no call uses more of.  A smaller one (or none) is taken as
+ * it is: the calls then split their work less. */
+#define QGEMV_WS_BYTES (64 << 20)
+
+/* A paged key and value cache: n_pages pages of page_size slots, each slot
+ * holding `heads` rows of head_dim values of `type` (QGEMV_TYPE_F16 or _BF16).
+ * Value e of head h in slot t of page p is at element
+ * p * page_stride + t * token_stride + h * head_stride + e of k and of v, so
+ * slots-major and heads-major pools are both described.  k, v: 16-byte
+ * aligned; strides: multiples of 8 elements; head_dim: a multiple of 8, at
+ * most QGEMV_HEAD_DIM_MAX; page_size: any, at most 65536.  The structure is a
+ * host structure, read during the call only. */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t page_stride, token_stride, head_stride;
+    int32_t n_pages, page_size, heads, head_dim, type;
+} qgemv_kv_cache;
+
+/* Rotates the first rot_dim values of every q and k head by the token's
+ * position and puts k and v into the cache.  For i < rot_dim / 2, with
+ * a = pos[t] * inv_freq[i] formed in 64 bits and reduced there (positions may
+ * be far), c = cos a and s = sin a:
+ *     (x_i, x_j) -> (x_i c - x_j s, x_j c + x_i s)
+ * where (i, j) are the i-th pair of `style`; the other values of a head are
+ * copied.  Arithmetic is fp32, rounded once to the cache's type.
+ *   q: [T][ldq], q_heads heads of head_dim each; NULL with q_heads = 0 for
+ *      none.  k, v: [T][ldk], [T][ldv], the cache's heads.  All of in_type,
+ *      16-byte aligned, with rows of a multiple of 16 bytes.
+ *   pos: int32 [T]; slots: int64 [T], page * page_size + slot in the page; a
+ *      token whose slot is negative or past the pool is not stored (its q is
+ *      still written).  Slots of one call must differ.
+ *   inv_freq: fp32 [rot_dim / 2] (NULL if rot_dim is 0); rot_dim even.
+ *   q_out: [T][ldqo] of the cache's type, 16-byte aligned rows. */
+qgemv_status qgemv_rope_append(const qgemv_kv_cache* cache, int64_t T, int in_type,
+                               const void* q, int64_t ldq, int q_heads, const void* k,
+                               int64_t ldk, const void* v, int64_t ldv, const int32_t* pos,
+                               const int64_t* slots, const float* inv_freq, int rot_dim,
+                               int style, void* q_out, int64_t ldqo, qgemv_stream_t stream);
+
+/* Attention of B sequences over a paged cache.  Sequence b brings the queries
+ * q_start[b] .. q_start[b + 1] - 1 (n of them) and owns keys 0 .. kv_len[b] - 1,
+ * the last n of which are the queries' own tokens (append first); key j is in
+ * page table[b][j / page_size].  Query i of the sequence, at p = kv_len[b] - n
+ * + i, sees key j if j <= p and (window <= 0 or p - j < window or j < sinks).
+ * With x_j = scale * (q . k_j) over the seen keys and m their largest:
+ *     l = sum exp(x_j - m),   out = sum exp(x_j - m) v_j / l,   lse = m + ln l
+ * A query that sees no key (or none whose score is above -inf) gets out = 0
+ * and lse = -inf.  Keys that a query does not see have no part in its result,
+ * whatever their slots hold, infinities and NaN included.  Query head h reads
+ * cache head h / (q_heads / heads).  Scores, m, l and sums are fp32; the
+ * weights exp(x - m) are rounded to the cache's type for the matrix cores.
+ *   q: [T][ldq] of the cache's type, q_heads heads of head_dim; 16-byte rows.
+ *   q_start: int32 [B + 1], kv_len: int32 [B]; starts are held to [0, T] and
+ *      to their order.
+ *   max_q: at least the most queries of a sequence (rows past it are not
+ *      written); max_kv: the longest kv_len expected, used only to choose how
+ *      the work is split.
+ *   table: int32 [B][ldt]; a page number outside the pool, or a page past
+ *      column ldt, means that its keys are absent: they are seen by no query.
+ *      Pages that no query sees may so be given back and marked -1.
+ *   out: [T][ldo] of out_type; rows of whole 16 bytes.  lse: fp32 [T][q_heads]
+ *      or NULL.
+ *   ws: ws_bytes of 16-byte aligned device memory for the parts of long rows
+ *      (NULL with 0 for none), free again when the call's work is done. */
+qgemv_status qgemv_paged_attn(const qgemv_kv_cache* cache, const void* q, int64_t T, int64_t ldq,
+                              int q_heads, const int32_t* q_start, const int32_t* kv_len, int B,
+                              int max_q, int64_t max_kv, const int32_t* table, int64_t ldt,
+                              float scale, int window, int sinks, void* out, int out_type,
+                              int64_t ldo, float* lse, void* ws, int64_t ws_bytes,
+                              qgemv_stream_t stream);
+
+/* Row quantisation to int8 with one scale per row (token of an activation, or
+ * output channel of a weight): amax = max|x_k| over the row; amax == 0 -> scale
+ * 0 and codes 0; otherwise sx = amax / 127 (IEEE fp32 division) and q_k =
+ * clamp(round_half_away(x_k / sx), -127, 127) (IEEE division), as
+ * qgemv_quantize_act does per block.  x: x_type [M][ldx], K valid columns,
+ * aligned to its elements; q: int8 [M][ldq], 16-byte aligned, ldq a multiple
+ * of 16 and >= K; codes from K to the next multiple of 16 are written as zero.
+ * sx: fp32 [M]. */
+qgemv_status qgemv_quantize_rows(const void* x, int x_type, int64_t M, int64_t K, int64_t ldx,
+                                 int8_t* q, int64_t ldq, float* sx, qgemv_stream_t stream);
+
+/* y[m][n] = sx[m] * sw[n] * sum_k q[m][k] * w[n][k] (+ bias[n]), the sum exact
+ * in int32, the rest fp32, rounded once to y_type; any M >= 0.
+ *   w: int8 [N][ldw], q: int8 [M][ldq]; 16-byte aligned, strides multiples of
+ *      16 and >= K; what lies between K and a row's end is not used.
+ *   sw, bias: fp32 [N] (bias may be NULL); sx: fp32 [M]; y: [M][ldy], aligned
+ *      to its elements, ldy >= N.
+ *   ws: as for qgemv_paged_attn, for the parts of sums split over K. */
+qgemv_status qgemm_w8a8(const int8_t* w, int64_t ldw, const float* sw, int64_t N, int64_t K,
+                        int64_t M, const int8_t* q, int64_t ldq, const float* sx,
+                        const float* bias, void* y, int y_type, int64_t ldy, void* ws,
+                        int64_t ws_bytes, qgemv_stream_t stream);
+/* qgemv_quantize_rows of x into q and sx, then qgemm_w8a8 on them, equal to
+ * the two calls bit for bit; q and sx receive the codes and scales. */
+qgemv_status qgemm_quantize_w8a8(const int8_t* w, int64_t ldw, const float* sw, int64_t N,
+                                 int64_t K, int64_t M, const void* x, int x_type, int64_t ldx,
+                                 int8_t* q, int64_t ldq, float* sx, const float* bias, void* y,
+                                 int y_type, int64_t ldy, void* ws, int64_t ws_bytes,
+                                 qgemv_stream_t stream);
 
 #ifdef __cplusplus
 }

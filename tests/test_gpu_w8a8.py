@@ -1,0 +1,153 @@
+"""Row quantisation and the int8 product against 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, host, say
+from layer_ref import TYPE_ID, TYPES, f64, product, quantise_rows, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import block_quantized_gemv_w4a8_amd as qg
+    return qg
+
+
+def up16(k):
+    return -(-k // 16) * 16
+
+
+def codes(g, rows, K, extra=0):
+    """Codes with what lies past K filled with other codes, which must not count."""
+    return g.integers(-128, 128, (rows, up16(K) + extra)).astype(np.int8)
+
+
+def one(qg, M, N, K, kind="fp32", bias=False, ws=True, extra=0, ldy=0, seed=0, full=False):
+    say("w8a8", M, N, K, kind, bias, ws, extra, ldy)
+    g = np.random.default_rng(seed + M + 7 * N + 31 * K)
+    q, w = codes(g, M, K, extra), codes(g, N, K, 2 * extra)
+    if full:
+        q[:], w[:] = -128, -128
+    sx, sw = (g.uniform(1e-4, 1e-2, n).astype(np.float32) for n in (M, N))
+    sx[M // 2] = 0
+    b = g.standard_normal(N).astype(np.float32) if bias else None
+    t = [None if a is None else torch.from_numpy(a).to(DEV) for a in (w, sw, q, sx, b)]
+    ld = ldy or N
+    y = torch.full((M, ld), float("nan"), dtype=TYPES[kind], device=DEV)
+    buf = torch.randint(0, 255, (qg.QGEMV_WS_BYTES,), dtype=torch.uint8, device=DEV) if ws else None
+    qg.qgemm_w8a8(t[0], w.shape[1], t[1], N, K, M, t[2], q.shape[1], t[3], t[4], y, TYPE_ID[kind], ld, buf, qg.QGEMV_WS_BYTES if ws else 0)
+    torch.cuda.synchronize()
+    ref, tol = product(q[:, :K], sx, w[:, :K], sw, b, kind)
+    within(f64(y)[:, :N], ref, tol, "y")
+    assert torch.isnan(y[:, N:]).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 15, 16, 17, 31, 33, 48, 63, 64, 65, 100, 127, 129, 200, 257, 300])
+@pytest.mark.parametrize("N,K", [(1, 1), (5, 15), (64, 64), (130, 257), (257, 891), (300, 1040), (96, 4097)])
+def test_sizes(qg, M, N, K):
+    one(qg, M, N, K)
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 5, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 192, 255, 256, 511, 513, 1023, 1025])
+@pytest.mark.parametrize("M", [1, 20, 90, 260])
+def test_depths(qg, K, M):
+    one(qg, M, 70, K)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M", [1, 7, 40, 150, 520])
+def test_types_bias_and_strides(qg, kind, bias, M):
+    one(qg, M, 203, 333, kind, bias, extra=48, ldy=211)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 14336), (16, 896, 4864), (40, 1000, 14336), (130, 512, 14336), (700, 1500, 1027), (64, 6000, 896)])
+@pytest.mark.parametrize("ws", [False, True])
+def test_larger(qg, M, N, K, ws):
+    one(qg, M, N, K, "bf16", ws=ws)
+
+
+def test_a_small_workspace_is_taken_as_it_is(qg):
+    g = np.random.default_rng(3)
+    M, N, K = 70, 130, 9000
+    q, w = codes(g, M, K), codes(g, N, K)
+    s = np.ones(N, np.float32)
+    d = [torch.from_numpy(a).to(DEV) for a in (w, s, q, s[:M])]
+    want = torch.from_numpy((q[:, :K].astype(np.int64) @ w[:, :K].T.astype(np.int64)).astype(np.float32)).to(DEV)
+    for size in (0, 16, 1000, 70 * 130 * 4, 300 * 1024, 1 << 22):
+        say("w8a8 workspace", size)
+        ws = torch.zeros(size + 256, dtype=torch.uint8, device=DEV)
+        y = torch.empty(M, N, device=DEV)
+        qg.qgemm_w8a8(d[0], w.shape[1], d[1], N, K, M, d[2], q.shape[1], d[3], None, y, 0, N, ws if size else None, size)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and not ws[size:].any()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_largest_sums(qg, M):
+    """Every code -128 at the largest K: the sum is 128 * 128 * K < 2^31."""
+    one(qg, M, 40, qg.QGEMV_W8A8_K_MAX, full=True)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("M,K,ldx", [(1, 1, 1), (1, 4096, 4096), (3, 15, 15), (5, 891, 891), (7, 896, 904), (2, 14336, 14336), (33, 1000, 1003), (4, 40001, 40001)])
+def test_quantise_rows(qg, kind, M, K, ldx):
+    say("quantise rows", kind, M, K, ldx)
+    g = np.random.default_rng(M * K)
+    x = g.standard_normal((M, ldx)).astype(np.float32)
+    x[:, : max(1, K // 50)] *= 30
+    x[:, K:] = np.inf
+    if M > 2:
+        x[1, :K] = 0
+        x[2, :K] = np.round(x[2, :K] * 2) / 2  # ties: 63.5 of them make the scale 1/2
+        x[2, 0] = 63.5
+    t = torch.from_numpy(x).to(TYPES[kind]).to(DEV)
+    ld = up16(K) + 16
+    q = torch.full((M, ld), 99, dtype=torch.int8, device=DEV)
+    sx = torch.full((M,), float("nan"), device=DEV)
+    qg.qgemv_quantize_rows(t, TYPE_ID[kind], M, K, ldx, q, ld, sx)
+    rq, rs = quantise_rows(t.float().cpu().numpy()[:, :K])
+    assert np.array_equal(host(sx), rs)
+    got = host(q)
+    assert np.array_equal(got[:, :K], rq) and not got[:, K:up16(K)].any() and (got[:, up16(K):] == 99).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 8, 33, 64, 65, 300])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,K", [(300, 1024), (77, 891), (64, 5000)])
+def test_quantised_in_the_call_is_the_two_calls(qg, M, kind, N, K):
+    say("quantise and product", M, kind, N, K)
+    g = np.random.default_rng(M)
+    x = torch.from_numpy(g.standard_normal((M, K)).astype(np.float32)).to(TYPES[kind]).to(DEV)
+    w, sw = torch.from_numpy(codes(g, N, K)).to(DEV), torch.rand(N, device=DEV)
+    ld = up16(K)
+    ws = torch.empty(qg.QGEMV_WS_BYTES, dtype=torch.uint8, device=DEV)
+    out = []
+    for fused in (False, True):
+        q = torch.full((M, ld), 99, dtype=torch.int8, device=DEV)
+        sx, y = torch.full((M,), float("nan"), device=DEV), torch.empty(M, N, dtype=TYPES[kind], device=DEV)
+        if fused:
+            qg.qgemm_quantize_w8a8(w, ld, sw, N, K, M, x, TYPE_ID[kind], K, q, ld, sx, None, y, TYPE_ID[kind], N, ws, qg.QGEMV_WS_BYTES)
+        else:
+            qg.qgemv_quantize_rows(x, TYPE_ID[kind], M, K, K, q, ld, sx)
+            qg.qgemm_w8a8(w, ld, sw, N, K, M, q, ld, sx, None, y, TYPE_ID[kind], N, ws, qg.QGEMV_WS_BYTES)
+        torch.cuda.synchronize()
+        out.append((q, sx, y))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(qg):
+    """Rows of codes more than 2^32 bytes apart from the first."""
+    ld, N, K = 2**30 + 2**12, 5, 200
+    buf = torch.empty(ld * (N - 1) + 4096, dtype=torch.int8, device=DEV)
+    w = buf.as_strided((N, K), (ld, 1))
+    w.copy_(torch.randint(-127, 128, (N, K), device=DEV).to(torch.int8))
+    for M in (1, 70):
+        say("w8a8 past 32 bits", M)
+        q = torch.randint(-127, 128, (M, 208), device=DEV).to(torch.int8)
+        y = torch.empty(M, N, device=DEV)
+        qg.qgemm_w8a8(w, ld, torch.ones(N, device=DEV), N, K, M, q, 208, torch.ones(M, device=DEV), None, y, 0, N)
+        assert np.array_equal(host(y), host(q)[:, :K].astype(np.int64) @ host(w).astype(np.int64).T)
