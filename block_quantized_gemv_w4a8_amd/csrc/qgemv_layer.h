@@ -39,6 +39,17 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
         *reinterpret_cast<uint4*>(p + 4) = *reinterpret_cast<const uint4*>(e + 4);
 }
 
+// Four values in one store, each rounded once (to nearest even).  p is aligned
+// to the four.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&f)[4]) {
+    alignas(16) T e[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) e[i] = (T)f[i];
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
+}
+
 // Calls f with a value of the element type `type` names.
 template <typename F>
 inline void with_type(int type, F f) {
@@ -116,5 +127,6 @@ struct W8A8Args {
     int64_t ws_bytes;
 };
 hipError_t launch_w8a8(const W8A8Args& a, hipStream_t st);
+hipError_t launch_quantize_w8a8(const RowsArgs& r, const W8A8Args& a, hipStream_t st);
 
 }  // namespace qgemv

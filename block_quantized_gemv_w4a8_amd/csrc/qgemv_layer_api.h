@@ -223,8 +223,7 @@ qgemv_status qgemm_quantize_w8a8(const int8_t* w, int64_t ldw, const float* sw, 
     if (st != QGEMV_OK) return st;
     if ((st = check_rows(name, r)) != QGEMV_OK) return st;
     if ((st = check_device()) != QGEMV_OK) return st;
-    st = launched(qgemv::launch_quantize_rows(r, (hipStream_t)stream), name);
-    return st != QGEMV_OK ? st : launched(qgemv::launch_w8a8(a, (hipStream_t)stream), name);
+    return launched(qgemv::launch_quantize_w8a8(r, a, (hipStream_t)stream), name);
 }
 
 }  // extern "C"
