@@ -167,8 +167,13 @@ struct Tile {
     static_assert(WGS >= 1 && (RING - 1) * LOADS < 60, "a ring that fits, and its loads in flight");
 };
 
+// A value of y in fp32.  (It is hidden from the compiler, which would otherwise
+// join the last step and the rounding to fp16 in some of the kernels, and the
+// same sums would give other bits there.)
 __device__ __forceinline__ float y_value(int acc, float sx, float sw, float bias) {
-    return (float)acc * sx * sw + bias;
+    float f = (float)acc * sx * sw + bias;
+    asm("" : "+v"(f));
+    return f;
 }
 
 // Four channels of a token, of which `left` are there; `to` needs no alignment
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tile<BM, BN, WM, WN, RING>::WGS * WM
         tn = (id - gi * group) / rows;
     };
 
-    // What is loaded, up to two stages ahead of what is multiplied: this lane's
+    // What is loaded, up to a ring ahead of what is multiplied: this lane's
     // chunk of each load of a stage, as an offset in the tile's rows of one
     // matrix (the launcher holds them below 2^32).
     const int8_t *base_w, *base_q;

@@ -197,3 +197,38 @@ def test_pools_past_32_bits(qg):
         qg.qgemv_paged_attn(qg.kv_cache(k, v), q, n, 64, 1, start, lens, 1, n, 45, table, 3, 0.125, 0, 0, out, 2, 64)
         o, tol, _, _ = attend(f64(q)[:, None], kk, vv, np.arange(45 - n, 45), 0, 0, 0.125, "bf16", "bf16")
         within(f64(out)[:, None], o, tol)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 32, 128])
+def test_pages_that_end_inside_a_run(qg, D, page):
+    """Whole runs of keys by one address and others key by key, with pages that end, that
+    are absent and that hold fewer keys than a run, in both kernels."""
+    one(qg, [(1, 700), (3, 129), (2, 16 * 33)], 4, 2, D, page=page, bad_ids={(0, 2): -1, (2, 5): 10**6})
+    one(qg, [(60, 300), (17, 17)], 4, 2, D, page=page, bad_ids={(0, 1): -1})
+
+
+@pytest.mark.parametrize("G", [1, 3, 8, 32, 40])
+@pytest.mark.parametrize("window", [0, 50])
+def test_group_sizes_at_the_border_of_the_kernels(qg, G, window):
+    """32 rows are the most of the single-token kernel."""
+    for n in (1, 32 // G or 1, 32 // G + 1):
+        one(qg, [(n, 200), (1, 70)], 2 * G, 2, 64, window=window, sinks=3, max_q=n)
+
+
+def test_tails_that_hold_nan_are_not_read(qg):
+    """What a page holds past the sequence's end, NaN or zeros, does not change a bit."""
+    for n, L in ((1, 37), (50, 101)):
+        say("attn tails", n, L)
+        k, v = (torch.randn(2, 64, 2, 128, device=DEV).bfloat16() for _ in range(2))
+        q = torch.randn(n, 4 * 128, device=DEV).bfloat16()
+        table = torch.tensor([[1, 0]], dtype=torch.int32, device=DEV)
+        start, lens = (torch.tensor(t, dtype=torch.int32, device=DEV) for t in ([0, n], [L]))
+        out = []
+        for tail in (0.0, float("nan")):
+            for t in (k, v):
+                t[int(table[0, L // 64]), L % 64:] = tail
+            o = torch.zeros(n, 4 * 128, device=DEV)
+            qg.qgemv_paged_attn(qg.kv_cache(k, v), q, n, 512, 4, start, lens, 1, n, L, table, 2, 0.1, 0, 0, o, 0, 512)
+            out.append(o)
+        assert torch.equal(*out) and out[0].abs().max() > 0

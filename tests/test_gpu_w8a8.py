@@ -151,3 +151,92 @@ def test_offsets_past_32_bits(qg):
         y = torch.empty(M, N, device=DEV)
         qg.qgemm_w8a8(w, ld, torch.ones(N, device=DEV), N, K, M, q, 208, torch.ones(M, device=DEV), None, y, 0, N)
         assert np.array_equal(host(y), host(q)[:, :K].astype(np.int64) @ host(w).astype(np.int64).T)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(2100, 9001, 300), (2047, 9216, 128), (1300, 7170, 1025), (900, 3500, 200)])
+def test_more_tiles_than_the_device_holds(qg, kind, M, N, K):
+    """Workgroups that go on from tile to tile, whole ones and ones at the edges."""
+    say("w8a8 many tiles", kind, M, N, K)
+    g = torch.Generator(device=DEV).manual_seed(K)
+    ld = up16(K)
+    q, w = (torch.randint(-128, 128, (n, ld), generator=g, device=DEV, dtype=torch.int8) for n in (M, N))
+    sx, sw = (2.0 ** torch.randint(-9, -5, (n,), generator=g, device=DEV).float() for n in (M, N))
+    b = torch.randint(-8, 8, (N,), generator=g, device=DEV).float()
+    y = torch.full((M, N), float("nan"), dtype=TYPES[kind], device=DEV)
+    qg.qgemm_w8a8(w, ld, sw, N, K, M, q, ld, sx, b, y, TYPE_ID[kind], N)
+    # sums below 2^24, powers of two and small whole numbers: fp32 arithmetic on them is exact
+    # for these K, and a value is rounded once
+    ref = (torch.mm(q[:, :K].double(), w[:, :K].double().t().contiguous()) * sx.double()[:, None] * sw.double() + b.double()).to(TYPES[kind])
+    assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 64, 14000), (100, 200, 9000), (300, 130, 12345), (600, 4096, 14336)])
+def test_split_sums_are_the_whole_ones(qg, M, N, K):
+    """Whole sums do not depend on how they are split: with and without a workspace, bit for bit."""
+    g = np.random.default_rng(K)
+    q, w = torch.from_numpy(codes(g, M, K)).to(DEV), torch.from_numpy(codes(g, N, K)).to(DEV)
+    sx, sw = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+    ws = torch.randint(0, 255, (qg.QGEMV_WS_BYTES,), dtype=torch.uint8, device=DEV)
+    out = []
+    for size in (0, qg.QGEMV_WS_BYTES):
+        say("w8a8 split", M, N, K, size)
+        y = torch.full((M, N), float("nan"), dtype=torch.float16, device=DEV)
+        qg.qgemm_w8a8(w, up16(K), sw, N, K, M, q, up16(K), sx, None, y, 1, N, ws if size else None, size)
+        out.append(y)
+    assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 600])
+@pytest.mark.parametrize("K", [100, 512, 513, 2048, 2049, 8192, 8200, 16384, 16500, 32768, 33000])
+def test_quantised_in_the_call_over_depths(qg, M, K):
+    """Each way that a row is read, and the limits of the quantisation in the product's launch."""
+    say("quantise and product, depth", M, K)
+    g = np.random.default_rng(M + K)
+    N = 40
+    x = torch.from_numpy(g.standard_normal((M, K + 3)).astype(np.float32)).to(DEV)
+    w, sw = torch.from_numpy(codes(g, N, K)).to(DEV), torch.rand(N, device=DEV)
+    ld = up16(K)
+    q = torch.full((M, ld + 16), 99, dtype=torch.int8, device=DEV)
+    sx, y = torch.empty(M, device=DEV), torch.empty(M, N, device=DEV)
+    qg.qgemm_quantize_w8a8(w, ld, sw, N, K, M, x, 0, K + 3, q, ld + 16, sx, None, y, 0, N)
+    rq, rs = quantise_rows(x.cpu().numpy()[:, :K])
+    assert np.array_equal(host(sx), rs) and np.array_equal(host(q)[:, :K], rq)
+    assert not host(q)[:, K:ld].any() and (host(q)[:, ld:] == 99).all()
+    ref, tol = product(rq, rs, host(w)[:, :K], host(sw), None, "fp32")
+    within(f64(y), ref, tol, "y")
+
+
+def test_on_another_stream_and_in_a_graph(qg):
+    """One product of each kind (a token, a few, a split one, tiles), captured on a side
+    stream: every replay is the eager result, with eager work between."""
+    sizes = [(1, 300, 1024), (9, 300, 1024), (40, 300, 9000), (300, 500, 700)]
+    ws = torch.empty(qg.QGEMV_WS_BYTES, dtype=torch.uint8, device=DEV)
+    g = np.random.default_rng(0)
+    cases = []
+    for M, N, K in sizes:
+        w = torch.from_numpy(codes(g, N, K)).to(DEV)
+        cases.append((M, N, K, w, torch.rand(N, device=DEV), torch.empty(M, K, device=DEV), torch.zeros(M, up16(K), dtype=torch.int8, device=DEV),
+                      torch.zeros(M, device=DEV), torch.zeros(M, N, device=DEV)))
+
+    def step():
+        for M, N, K, w, sw, x, q, sx, y in cases:
+            qg.qgemm_quantize_w8a8(w, up16(K), sw, N, K, M, x, 0, K, q, up16(K), sx, None, y, 0, N, ws, qg.QGEMV_WS_BYTES)
+
+    say("w8a8 graph")
+    graph = torch.cuda.CUDAGraph()
+    for c in cases:
+        c[5].normal_()
+    step()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        step()
+    for i in range(3):
+        for c in cases:
+            c[5].normal_()
+            c[8].zero_()
+        graph.replay()
+        got = [c[8].clone() for c in cases]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c[8]) and a.abs().max() > 0 for a, c in zip(got, cases))
