@@ -384,12 +384,21 @@ struct Rows {
 // key.
 template <int DP, int KT>
 struct Pages {
-    int first = 0, page = -1;              // the lane's column is first + lane
+    int first = -64, page = -1;            // the lane's column is first + lane
     unsigned long long valid = 0;          // columns with a page of the pool
-    bool loaded = false;
     int j0;                                // the tile: its first key
     bool runs;                             // whether scalars do
     int64_t off;                           // byte offset of key `lane`, -1 where it is not there
+
+    // The table's first columns, asked for before anything else is known (lengths
+    // are on their way meanwhile), and their arrival.  (Chunks gain 1.5 us of 49 by
+    // it; single tokens gain nothing.)
+    __device__ __forceinline__ void ask(const AttnDev& a, const int32_t* table) {
+        const int lane = threadIdx.x & 63;
+        first = 0;
+        if (lane < a.ldt) page = table[lane];
+    }
+    __device__ __forceinline__ void arrive(const AttnDev& a) { valid = __ballot(page >= 0 && page < a.n_pages); }
 
     // Takes up the tile at key j; returns which of its keys are there.
     __device__ __forceinline__ unsigned long long tile(const AttnDev& a, const Span& s, const int32_t* table,
@@ -399,11 +408,10 @@ struct Pages {
         off = -1;
         const int c0 = a.page_shift >= 0 ? j0 >> a.page_shift : j0 / a.page_size;
         const int c1 = a.page_shift >= 0 ? (j0 + KT - 1) >> a.page_shift : (j0 + KT - 1) / a.page_size;
-        if (!loaded || c0 < first || c1 >= first + 64) {
+        if (c0 < first || c1 >= first + 64) {
             first = c0;
             page = first + lane < a.ldt ? table[first + lane] : -1;
-            loaded = true;
-            valid = __ballot(page >= 0 && page < a.n_pages);   // (the wait for the page is here, not at every tile)
+            arrive(a);   // (the wait for the page is here, not at every tile)
         }
         const unsigned long long need = (2ull << (c1 - c0)) - 1;
         runs = a.runs && j0 + KT <= s.limit && (valid >> (c0 - first) & need) == need;
@@ -476,9 +484,11 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
     const int rest = blockIdx.x / a.heads;
     const int part = rest % a.splits, row_tile = a.row_tiles - 1 - rest / a.splits;
     const int b = blockIdx.y;
+    const int32_t* table = a.table + b * a.ldt;
+    Pages<DP, KT> pages;
+    pages.ask(a, table);
     Span s;
     if (!make_span<KT, ROWS>(a, b, row_tile, part, s)) return;
-    const int32_t* table = a.table + b * a.ldt;
 
     // this lane's row, the last one of the block where it has none of its own
     const int first_row = row_tile * ROWS + 32 * wave, r = first_row + (lane & 31);
@@ -487,10 +497,10 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
     const bool active = first_row < r_end;
     R w;
     w.start(a, s, h, rc, first_row);
+    pages.arrive(a);
 
     const char* kbase = (const char*)((const T*)a.k + h * a.head_stride);
     const char* vbase = (const char*)((const T*)a.v + h * a.head_stride);
-    Pages<DP, KT> pages;
     auto load_tile = [&](int t, char* buf) -> unsigned long long {
         const unsigned long long there = pages.tile(a, s, table, tile_of(s, t) * KT);
         pages.template load<LOADS>(a, kbase, R::RPI * LOADS * wave, buf, L::fk);
@@ -583,9 +593,10 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDe
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, row32 = lane & 31;
     const int h = blockIdx.x % a.heads, part = blockIdx.x / a.heads, b = blockIdx.y;
+    const int32_t* table = a.table + b * a.ldt;
+    Pages<DP, KT> pages;
     Span s;
     if (!make_span<KT, ROWS>(a, b, 0, part, s)) return;
-    const int32_t* table = a.table + b * a.ldt;
     const int rows = (s.i1 + 1) * a.G;
     R w;
     w.start(a, s, h, min(row32, rows - 1), 0);
@@ -595,7 +606,6 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDe
     char* mine = lds + wave * RING;                     // K, K, V, V
     const int each = (s.t1 - s.t0 + NW - 1) / NW;
     const int t0 = min(s.t0 + wave * each, s.t1), t1 = min(t0 + each, s.t1);
-    Pages<DP, KT> pages;
     auto take = [&](int t) { return pages.tile(a, s, table, tile_of(s, t) * KT); };
     auto load_k = [&](int slot) { pages.template load<LOADS>(a, kbase, 0, mine + slot * TILE, L::fk); };
     auto load_v = [&](int slot) { pages.template load<LOADS>(a, vbase, 0, mine + (2 + slot) * TILE, L::fv); };
@@ -688,24 +698,42 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
     const int d = 4 * (threadIdx.x % LANES), b = blockIdx.y;
     const int i = r / a.q_heads, hq = r - i * a.q_heads, h = hq / a.G;
     if (i >= a.max_q || d >= a.D) return;
+    // the place of the row's parts needs its sequence's start only, and the first
+    // parts are asked for before it is known how many there are
+    const int s0 = min(max(a.q_start[b], 0), a.T);
+    const int64_t tok = s0 + i, row = tok * a.q_heads + hq;
+    const float* ml = a.part_ml + 2 * row * a.splits;
+    const float* po = a.part_o + row * a.splits * a.D + d;
+    constexpr int AHEAD = 8;
+    float m[AHEAD], l[AHEAD];
+    f32x4v v[AHEAD];
+#pragma unroll
+    for (int w = 0; w < AHEAD; w++) {
+        if (tok >= a.T || w >= a.splits) continue;
+        m[w] = ml[2 * w];
+        l[w] = ml[2 * w + 1];
+        v[w] = *reinterpret_cast<const f32x4v*>(po + (int64_t)w * a.D);
+    }
     Span s;
     const int row_tile = (i * a.G + hq - h * a.G) / ROWS;
     if (!make_span<KT, ROWS>(a, b, row_tile, 0, s) || i >= s.n || s.parts == 1) return;
-    const int64_t tok = s.s0 + i, row = tok * a.q_heads + hq;
-    const float* ml = a.part_ml + 2 * row * a.splits;
-    const float* po = a.part_o + row * a.splits * a.D + d;
     float top = -INFINITY, sum = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int w = 0; w < s.parts; w++) top = fmaxf(top, ml[2 * w]);
-#pragma unroll 8
-    for (int w = 0; w < s.parts; w++) {
-        const float mw = ml[2 * w];
-        const float fix = mw == top ? 1.f : exp2f(mw - top);
-        const f32x4v v = *reinterpret_cast<const f32x4v*>(po + (int64_t)w * a.D);
-        sum += ml[2 * w + 1] * fix;
 #pragma unroll
-        for (int c = 0; c < 4; c++) f[c] += v[c] * fix;
-    }
+    for (int w = 0; w < AHEAD; w++)
+        if (w < s.parts) top = fmaxf(top, m[w]);
+    for (int w = AHEAD; w < s.parts; w++) top = fmaxf(top, ml[2 * w]);
+    auto join = [&](float mw, float lw, const f32x4v& vw) {
+        const float fix = mw == top ? 1.f : exp2f(mw - top);
+        sum += lw * fix;
+#pragma unroll
+        for (int c = 0; c < 4; c++) f[c] += vw[c] * fix;
+    };
+#pragma unroll
+    for (int w = 0; w < AHEAD; w++)
+        if (w < s.parts) join(m[w], l[w], v[w]);
+#pragma unroll 4
+    for (int w = AHEAD; w < s.parts; w++)
+        join(ml[2 * w], ml[2 * w + 1], *reinterpret_cast<const f32x4v*>(po + (int64_t)w * a.D));
     const float inv = row_scale(sum);
 #pragma unroll
     for (int c = 0; c < 4; c++) f[c] *= inv;
