@@ -465,7 +465,15 @@ struct Pages {
     }
 };
 
-// Many rows: NW waves of 32 rows each, which share every tile of KT keys.
+// Many rows: NW waves of 32 rows each, which share every tile of KT keys, the next
+// tile on its way while one is used.  A row's 32 weights of a tile cost a lane's
+// vector pipe about what its matrix instructions cost the matrix pipe (206 and 32
+// instructions a tile of 64 keys at 128 dimensions), and waves of two workgroups
+// a SIMD share the two: 8192 tokens of 32 heads on 8, causal, take 567 us, 970
+// TFLOP/s.  (With the LDS places formed for each read, 302 vector instructions,
+// it took 629; with the scores of 32 keys formed beside the weights of the 32
+// before, 660.)  Batches of short chunks are bound by the tiles' chain of loads,
+// scores and weights: 43 us for nine sequences with a window of 1024.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
     typedef Rows<T, DP, KT> R;
@@ -580,7 +588,9 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
 // At most 32 rows: each of NW waves takes a run of the tiles.  Its ring holds two
 // K and two V tiles; a tile's K makes room for the K after next as soon as the
 // scores are formed, and V likewise, so that three of the four are always on
-// their way.
+// their way.  Bound by the cache's bytes: 64 sequences of up to 8192 keys take 313
+// us, 5.5 TB/s (361 with whole tiles in turn, two to a wave); one short sequence
+// is bound by the chain of lengths, pages, keys, 9.6 us.
 template <typename T, typename TO, int DP, int NW>
 __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDev a) {
     constexpr int KT = 32, ROWS = 32;
@@ -691,7 +701,8 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDe
 }
 
 // Joins the parts of the rows whose keys were split: LANES lanes a row, four
-// dimensions each.
+// dimensions each, eight parts in flight (18 rows of 32 heads in five parts: 4.4
+// us, where a wave a row and part after part took 11.7).
 template <typename TO, int KT, int ROWS, int LANES>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
     const int r = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;  // query and head of the sequence
@@ -742,7 +753,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 }
 
 // How many parts the longest list of tiles is split into: as many as fill the
-// device once (`slots` workgroups), of at least min_tiles each.
+// device once (`slots` workgroups), of at least min_tiles each.  More parts than
+// that only cost the join (a window of 4096 over six sequences: five parts 25 us,
+// sixteen 43; nine sequences of chunks: one part 51 us, two 96).
 static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int64_t ws_bytes, void* ws) {
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);
     int64_t seen = max_kv;

@@ -62,7 +62,9 @@ __device__ __forceinline__ float row_top(float top, float* part) {
 }
 
 // One workgroup of W waves a row, which holds the row in CH chunks of 8 values
-// a thread and reads it once; CH = 0: a row of any length, read twice.
+// a thread and reads it once; CH = 0: a row of any length, read twice.  Bound by
+// the bytes where rows are many, by the way there and back where they are few
+// (one row of 4096: about 3 us, with two passes 8.8).
 template <typename T, int W, int CH>
 __global__ __launch_bounds__(64 * W) void k_quantize_rows(const T* __restrict__ x, int64_t K,
                                                           int64_t ldx, int8_t* __restrict__ q,
@@ -143,14 +145,25 @@ __device__ __forceinline__ i32x4 codes16(const int8_t* row, int64_t k, int64_t K
     return v;
 }
 
-// A tile of y by one workgroup of WM x WN waves: BM tokens, BN channels.
+// A tile of y by one workgroup of WM x WN waves: BM tokens, BN channels; the
+// workgroup goes on from tile to tile, and the next one's codes are on their way
+// while a tile's sums are scaled and stored.
 //
 // A stage holds 128 codes of every row of the tile: 16-byte chunk c of row r
 // sits at place c ^ (r / 2 % 8) of the row, so that the 16 rows of a
 // fragment's column of chunks fall on all banks.  Stages go from memory
 // straight to LDS, round a ring of RING.  A wave's sums are 32x32x32 tiles with
 // the tokens down and the channels across, so that a store has whole runs of
-// channels.
+// channels, and a token's runs are stored one after another (with the channels
+// down, 16-byte pieces of 32 rows a store, fp32 rows of odd length took 52 us
+// where runs take 33: 3539 x 7187 x 306).
+//
+// Large tiles are bound by the matrix cores at the clock that their power leaves:
+// 4096 x 28672 x 4096 takes 465 us, 2070 TOP/s (2110 is what the library's int8
+// product reaches, its sums unscaled); the matrix instructions alone, on the same
+// codes, run at 2870, and codes of zero at 2450.  Small ones are bound by the way
+// from memory to LDS, so they have more stages on their way: 64 x 4096 x 14336
+// with a ring of two 35 us, of four 20.
 template <int BM, int BN, int WM, int WN, int RING>
 struct Tile {
     static constexpr int WAVES = WM * WN;
@@ -465,7 +478,9 @@ __global__ __launch_bounds__(64 * WM * WN, (Tile<BM, BN, WM, WN, RING>::WGS * WM
 // Few tokens: a workgroup holds 16 channels and 16 MT tokens, and its waves take
 // the runs of 128 codes in turn.  Codes go from memory to registers, in which a
 // fragment of the 16x16x64 matrix instruction is 16 codes of one row a lane, U
-// runs in flight.  The waves' sums meet in LDS.
+// runs in flight.  The waves' sums meet in LDS.  Bound by the weights' bytes: 2 x
+// 4096 x 14336 takes 13.3 us, 4.4 TB/s (16 x 28672 x 4096, whose token codes are
+// as many again from L2, 33.6).
 template <typename TY, int MT, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 8 : 5) void k_w8a8_stream(const W8Dev a,
                                                                            TY* __restrict__ y) {
@@ -543,7 +558,8 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 8 : 5) void k_w8a8_stream(con
 // At most kTokenM rows, from x with their quantisation in the launch or (TX is
 // int8_t) from their codes: every workgroup forms the codes in its LDS (the
 // first one also writes them out) while its first weight codes are on their
-// way.  Otherwise as k_w8a8_stream.
+// way.  Otherwise as k_w8a8_stream.  1 x 28672 x 4096 takes 22.2 us from codes,
+// 5.3 TB/s, and 23.8 from x.
 constexpr int kTokenM = 2;
 
 template <typename TX, typename TY, int WAVES, int U>
@@ -661,7 +677,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_w8a8_token(const W8Dev a, const 
     put4(y + tok * a.ldy + c, v, a.N - c);
 }
 
-// Joins sums that were split over K: four channels of one token a thread.
+// Joins sums that were split over K: four channels of one token a thread, up to
+// eight parts in flight (16 parts of 40 x 4096: about 4 us with its launch).
 template <typename TY>
 __global__ __launch_bounds__(256) void k_w8a8_join(const W8Dev a, int parts, TY* __restrict__ y) {
     const uint32_t runs = (uint32_t)((a.N + 3) / 4), at = blockIdx.x * 256 + threadIdx.x;

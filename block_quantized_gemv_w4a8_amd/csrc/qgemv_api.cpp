@@ -270,7 +270,8 @@ const char* qgemv_build_info(void) {
            "two-block_tiles_mfma_i8_16x16x64(M<=8) "
            "block_dots=lds-rows,staged-stream,small_m_mfma_tiles "
            "fused=q4_k_swiglu_quantize,quantize_gemv,quantize_q4_k_swiglu multi=multi,quantize_multi(<=8) "
-           "stream_read=calibration K_max=32768 M_max=64";
+           "stream_read=calibration K_max=32768 M_max=64 "
+           "layer=rope_append,paged_attn(mfma_32x32x16),quantize_rows,w8a8(mfma_i8_32x32x32,16x16x64)";
 }
 
 const char* qgemv_last_error(void) { return g_last_error; }

@@ -484,7 +484,8 @@ qgemv_status qgemv_paged_attn(const qgemv_kv_cache* cache, const void* q, int64_
  * qgemv_quantize_act does per block.  x: x_type [M][ldx], K valid columns,
  * aligned to its elements; q: int8 [M][ldq], 16-byte aligned, ldq a multiple
  * of 16 and >= K; codes from K to the next multiple of 16 are written as zero.
- * sx: fp32 [M]. */
+ * sx: fp32 [M].  (Values are meant to be finite: an infinity makes the row's
+ * scale infinite, and a NaN's code means nothing.) */
 qgemv_status qgemv_quantize_rows(const void* x, int x_type, int64_t M, int64_t K, int64_t ldx,
                                  int8_t* q, int64_t ldq, float* sx, qgemv_stream_t stream);
 
