@@ -753,7 +753,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 }
 
 // How many parts the longest list of tiles is split into: as many as fill the
-// device once (`slots` workgroups), of at least min_tiles each.  More parts than
+// device once (`slots` workgroups), of at least min_tiles each (four tiles of the
+// many-row kernel: 2 x 178 queries over 2107 keys, one cache head, 24.7 us with
+// eight, 22.1 with four).  More parts than
 // that only cost the join (a window of 4096 over six sequences: five parts 25 us,
 // sixteen 43; nine sequences of chunks: one part 51 us, two 96).
 static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int64_t ws_bytes, void* ws) {
@@ -782,7 +784,7 @@ static void join(const AttnDev& d, hipStream_t st) {
 template <typename T, typename TO, int DP, int KT, int OCC>
 static void launch_many(AttnDev d, const AttnArgs& a, hipStream_t st) {
     constexpr int NW = 4, ROWS = 32 * NW;
-    split(d, a.max_kv, ROWS, KT, 8, 256 * OCC, a.ws_bytes, a.ws);
+    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC, a.ws_bytes, a.ws);
     launch_kernel(k_attn_many<T, TO, DP, KT, NW, OCC>,
                   dim3((unsigned)(d.heads * d.splits * d.row_tiles), (unsigned)d.B), dim3(64 * NW),
                   2 * 2 * KT * DP * 2, st, d);
