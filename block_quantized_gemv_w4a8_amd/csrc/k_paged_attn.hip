@@ -755,9 +755,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 // How many parts the longest list of tiles is split into: as many as fill the
 // device once (`slots` workgroups), of at least min_tiles each (four tiles of the
 // many-row kernel: 2 x 178 queries over 2107 keys, one cache head, 24.7 us with
-// eight, 22.1 with four).  More parts than
-// that only cost the join (a window of 4096 over six sequences: five parts 25 us,
-// sixteen 43; nine sequences of chunks: one part 51 us, two 96).
+// eight, 22.1 with four).  More parts than that only cost the join (a window of
+// 4096 over six sequences: five parts 25 us, sixteen 43; nine sequences of chunks:
+// one part 51 us, two 96).
 static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int64_t ws_bytes, void* ws) {
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);
     int64_t seen = max_kv;

@@ -240,3 +240,27 @@ def test_on_another_stream_and_in_a_graph(qg):
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c[8]) and a.abs().max() > 0 for a, c in zip(got, cases))
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0**-60, 2.0**-105, 2.0**-126, 2.0**100])
+def test_quantise_at_the_borders(qg, scale):
+    """Values half way between two codes, next to that, and at whole multiples of the scale,
+    for ordinary scales and ones at the ends of fp32: codes are those of the rounded quotient."""
+    say("quantise borders", scale)
+    g = np.random.default_rng(7)
+    rows = []
+    for i in range(40):
+        top = np.float32((127 if i % 4 == 0 else g.uniform(1, 200)) * scale)
+        d = np.float32(top / np.float32(127))
+        k = np.arange(0, 127, dtype=np.float64)
+        half, whole = ((np.float64(d) * t).astype(np.float32) for t in (k + 0.5, k))
+        row = np.concatenate([half, np.nextafter(half, np.float32(0)), np.nextafter(half, np.float32(np.inf)), whole,
+                              np.nextafter(whole, np.float32(np.inf)), (g.uniform(0, 1, 300) * top).astype(np.float32), [top]])
+        rows.append(np.minimum(row, top) * np.where(g.random(len(row)) < 0.5, -1, 1).astype(np.float32))
+    x = np.stack(rows).astype(np.float32)
+    M, K = x.shape
+    q = torch.zeros(M, up16(K), dtype=torch.int8, device=DEV)
+    sx = torch.empty(M, device=DEV)
+    qg.qgemv_quantize_rows(torch.from_numpy(x).to(DEV), 0, M, K, K, q, up16(K), sx)
+    rq, rs = quantise_rows(x)
+    assert np.array_equal(host(sx), rs) and np.array_equal(host(q)[:, :K], rq)
