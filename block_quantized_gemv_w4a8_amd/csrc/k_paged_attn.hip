@@ -757,8 +757,11 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 // many-row kernel: 2 x 178 queries over 2107 keys, one cache head, 24.7 us with
 // eight, 22.1 with four).  More parts than that only cost the join (a window of
 // 4096 over six sequences: five parts 25 us, sixteen 43; nine sequences of chunks:
-// one part 51 us, two 96).
-static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int64_t ws_bytes, void* ws) {
+// one part 51 us, two 96).  Long lists go on to `long_slots` in parts of four times
+// as many tiles, where a CU holds that many workgroups (64 dimensions: 2449
+// queries over 3695 keys, 14 heads on 2, one part 74.7 us, three 61.8).
+static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int long_slots,
+                  int64_t ws_bytes, void* ws) {
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);
     int64_t seen = max_kv;
     if (d.window > 0)
@@ -766,7 +769,8 @@ static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, i
     const int64_t tiles = std::max<int64_t>(1, (seen + kt - 1) / kt);
     const int64_t blocks = (int64_t)d.row_tiles * d.heads * d.B;
     const int64_t per = (int64_t)d.T * d.q_heads * (d.D + 2) * 4;
-    int64_t splits = std::min(slots / blocks, (tiles + min_tiles - 1) / min_tiles);
+    int64_t splits = std::max(std::min(slots / blocks, (tiles + min_tiles - 1) / min_tiles),
+                              std::min(long_slots / blocks, tiles / (4 * min_tiles)));
     splits = std::max<int64_t>(1, std::min(splits, std::min<int64_t>(ws_bytes, QGEMV_WS_BYTES) / per));
     d.splits = (int)splits;
     d.split_tiles = (int)((tiles + splits - 1) / splits);
@@ -784,7 +788,7 @@ static void join(const AttnDev& d, hipStream_t st) {
 template <typename T, typename TO, int DP, int KT, int OCC>
 static void launch_many(AttnDev d, const AttnArgs& a, hipStream_t st) {
     constexpr int NW = 4, ROWS = 32 * NW;
-    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC, a.ws_bytes, a.ws);
+    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC, DP == 64 ? 1024 : 0, a.ws_bytes, a.ws);
     launch_kernel(k_attn_many<T, TO, DP, KT, NW, OCC>,
                   dim3((unsigned)(d.heads * d.splits * d.row_tiles), (unsigned)d.B), dim3(64 * NW),
                   2 * 2 * KT * DP * 2, st, d);
@@ -792,7 +796,7 @@ static void launch_many(AttnDev d, const AttnArgs& a, hipStream_t st) {
 }
 template <typename T, typename TO, int DP, int NW>
 static void launch_few(AttnDev d, const AttnArgs& a, hipStream_t st) {
-    split(d, a.max_kv, 32, 32, 4 * NW, 256, a.ws_bytes, a.ws);
+    split(d, a.max_kv, 32, 32, 4 * NW, 256, 0, a.ws_bytes, a.ws);
     launch_kernel(k_attn_few<T, TO, DP, NW>, dim3((unsigned)(d.heads * d.splits), (unsigned)d.B),
                   dim3(64 * NW), NW * (4 * 32 * DP * 2 + 256), st, d);
     join<TO, 32, 32, DP / 4>(d, st);
