@@ -29,7 +29,7 @@ __device__ __forceinline__ void row8(const T* row, int64_t c, int64_t K, float (
     T e[8] = {};
     if (8 * c + 8 <= K) {
         __builtin_memcpy(e, row + 8 * c, sizeof e);
-    } else {
+    } else if (8 * c < K) {
 #pragma unroll
         for (int i = 0; i < 8; i++)
             if (8 * c + i < K) e[i] = row[8 * c + i];
@@ -89,9 +89,9 @@ __device__ __forceinline__ float row_top(float top, float* part) {
 
 // One workgroup of W waves a row, which holds the row in CH chunks of 8 values
 // a thread and reads it once; CH = 0: a row of any length, read twice.  Bound by
-// the codes' arithmetic where rows are many (4096 rows of 4096 bf16 values 14.5
-// us, 3.5 TB/s; with divisions 17.7), by the way there and back where they are
-// few (one row of 4096 2.6 us, with two passes 8.8).
+// the codes' arithmetic where rows are many (4096 rows of 4096 bf16 values 12.0
+// us, 4.2 TB/s; with chunks to spare 14.3, with divisions too 17.7), by the way
+// there and back where they are few (one row of 4096 2.4 us, with two passes 8.8).
 template <typename T, int W, int CH>
 __global__ __launch_bounds__(64 * W) void k_quantize_rows(const T* __restrict__ x, int64_t K,
                                                           int64_t ldx, int8_t* __restrict__ q,
@@ -140,10 +140,13 @@ hipError_t launch_quantize_rows(const RowsArgs& a, hipStream_t st) {
         // few rows: many threads a row; many rows: enough values a thread
         const bool many = a.M > 512;
         if (a.K <= 512) go(Int<1>{}, Int<1>{});
+        else if (a.K <= 1024 && many) go(Int<1>{}, Int<2>{});
         else if (a.K <= 2048 && many) go(Int<1>{}, Int<4>{});
         else if (a.K <= 2048) go(Int<4>{}, Int<1>{});
+        else if (a.K <= 4096 && many) go(Int<4>{}, Int<2>{});
         else if (a.K <= 8192 && many) go(Int<4>{}, Int<4>{});
         else if (a.K <= 8192) go(Int<16>{}, Int<1>{});
+        else if (a.K <= 16384) go(Int<16>{}, Int<2>{});
         else if (a.K <= 32768) go(Int<16>{}, Int<4>{});
         else go(Int<16>{}, Int<0>{});
     });
