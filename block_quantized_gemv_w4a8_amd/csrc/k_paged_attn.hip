@@ -325,14 +325,18 @@ struct Rows {
             m = mn;
         }
         const float mu = m == -INFINITY ? 0.f : m;
+        // (l takes a tile's weights at once: one by one those below half of its last
+        // bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is)
+        float sum = 0.f;
 #pragma unroll
         for (int n = 0; n < NX; n++)
 #pragma unroll
             for (int e = 0; e < 16; e++) {
                 const float w = __builtin_amdgcn_exp2f(fmaf(x[n][e], c2, -mu));
-                l += w;
+                sum += w;
                 pf[2 * n + e / 8][e % 8] = (T)w;
             }
+        l += sum;
     }
     // This lane's part of a transposing read: dimensions 32 d .. 32 d + 31, keys 8 w
     // + 4 half .. + 3 of sixteen.

@@ -1,0 +1,92 @@
+"""Attention over a paged cache: long rows of which one key holds almost all the weight."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, say
+from layer_ref import F32, HALF, TYPES, f64, rounded, within
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import block_quantized_gemv_w4a8_amd as qg
+    return qg
+
+
+class Problem:
+    """Sequences [(q [n, Hq, D], k [L, H, D], v)] of one type, in pages of 64 in reverse order."""
+
+    def __init__(self, qg, seqs, kind, window=0, sinks=0, scale=1.0):
+        self.qg, self.kind, self.window, self.sinks, self.scale = qg, kind, window, sinks, scale
+        self.Hq, self.D = seqs[0][0].shape[1:]
+        H = seqs[0][1].shape[1]
+        cols = [-(-k.shape[0] // PAGE) for _, k, _ in seqs]
+        self.pools = [torch.zeros(sum(cols), PAGE, H, self.D, dtype=TYPES[kind], device=DEV) for _ in range(2)]
+        table, used = torch.full((len(seqs), max(cols)), -1, dtype=torch.int32), sum(cols)
+        for b, (_, k, v) in enumerate(seqs):
+            for pool, x in zip(self.pools, (k, v)):
+                flat = torch.zeros(cols[b] * PAGE, H, self.D, dtype=TYPES[kind], device=DEV)
+                flat[:len(x)] = x
+                pool[used - cols[b]:used] = flat.view(-1, PAGE, H, self.D).flip(0)
+            table[b, :cols[b]] = torch.arange(used - 1, used - cols[b] - 1, -1)
+            used -= cols[b]
+        counts = [len(q) for q, _, _ in seqs]
+        self.q = torch.cat([q.reshape(len(q), -1) for q, _, _ in seqs]).to(TYPES[kind]).to(DEV)
+        self.T, self.B, self.max_q, self.max_kv = sum(counts), len(seqs), max(counts), max(len(k) for _, k, _ in seqs)
+        self.start = torch.tensor([0] + counts).cumsum(0).to(torch.int32).to(DEV)
+        self.lens = torch.tensor([len(k) for _, k, _ in seqs], dtype=torch.int32, device=DEV)
+        self.table = table.to(DEV)
+        self.cache = qg.kv_cache(*self.pools)
+        self.out = torch.full((self.T, self.Hq * self.D), 7.0, device=DEV)
+        self.lse = torch.full((self.T, self.Hq), 7.0, device=DEV)
+        #: bytes of the workspace that one part of every row takes
+        self.part = self.T * self.Hq * (self.D + 2) * 4
+
+    def run(self, ws=None, ws_bytes=0):
+        self.qg.qgemv_paged_attn(self.cache, self.q, self.T, self.Hq * self.D, self.Hq, self.start, self.lens, self.B, self.max_q,
+                                 self.max_kv, self.table, self.table.shape[1], self.scale, self.window, self.sinks, self.out,
+                                 self.qg.QGEMV_TYPE_F32, self.Hq * self.D, self.lse, ws, ws_bytes)
+        return self.out.view(self.T, self.Hq, self.D), self.lse
+
+
+def peaked(kind, Hq, gap, L=131072, D=64):
+    """One query whose key 5 scores `gap` above all the others, which score alike; half of
+    the dimensions are zero at the peak, so that they are the tail's alone."""
+    g = torch.Generator(device=DEV).manual_seed(int(gap * 10))
+    q = torch.zeros(1, Hq, D, device=DEV).to(TYPES[kind])
+    k = torch.zeros(L, 1, D, device=DEV).to(TYPES[kind])
+    q[..., 0], k[5, 0, 0] = 8, gap / 8
+    v = (torch.rand(L, 1, D, generator=g, device=DEV) + 0.5).to(TYPES[kind])
+    v[5, 0, :D // 2] = 0
+    return q, k, v
+
+
+def peaked_ref(q, k, v, kind):
+    """(out, tolerance, lse, tolerance).  A weight is rounded to the cache's type; the largest
+    of a tile that is not far below the maximum is 2^7 or more for fp16, so what is lost below
+    fp16's normal range is half of 2^-24 of that.  l takes the keys of a tile of 32 or 64 at
+    once, each lane summing 32 at most; the sums of v take sixteen a step, two roundings each."""
+    D, L = k.shape[2], k.shape[0]
+    x = f64(k)[:, 0] @ f64(q)[0, 0]
+    e = np.exp(x - x.max())
+    l, vv = e.sum(), f64(v)[:, 0]
+    out, lse = e @ vv / l, x.max() + np.log(l)
+    dx = (D + 3) * F32 * np.abs(x).max() + 8 * F32
+    lost = 2.0**-32 * vv.sum(0) / l if kind == "fp16" else 0.0
+    tol = rounded(out * (HALF[kind] + 2 * dx + (L / 8 + L / 32 + 64 + 8) * F32) + lost, out, "fp32")
+    return out, tol, lse, dx + (L / 32 + 64 + 8) * F32 + 4 * F32 * abs(lse)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("Hq", [1, 40])
+@pytest.mark.parametrize("gap", [16.8, 17.4, 18.5])
+def test_a_long_flat_tail_beside_a_peak_counts_in_lse(qg, kind, Hq, gap):
+    """131071 weights near 2^-25 of the largest: one by one they would leave an fp32 sum as it is."""
+    say("attn tail lse", kind, Hq, gap)
+    q, k, v = peaked(kind, Hq, gap)
+    _, lse = Problem(qg, [(q, k, v)], kind).run()
+    _, _, ref, tol = peaked_ref(q, k, v, kind)
+    within(f64(lse)[0], np.full(Hq, ref), tol, "lse")
