@@ -206,9 +206,14 @@ __device__ void put_row(const AttnDev& a, const Span& s, int part, int i, int hq
 }
 
 // The weights may grow to 2^kSlack of the running maximum's before o and l are
-// scaled: almost every tile after the first few then leaves them alone.  2^8
-// stays far inside fp16, and the weights' relative precision is the same.
+// scaled: almost every tile after the first few then leaves them alone.
 constexpr float kSlack = 8.f;
+// The maximum's own weight is 2^kLift.  fp16 ends at 2^16 and holds nothing below
+// 2^-24, and o takes the rounded weights where l takes the fp32 ones: with 1 for the
+// maximum, a tail of 131071 keys at 2^-25 of it was lost from o alone, 0.36% of the
+// row.  With 2^7 the slack ends at 2^15, and what is lost is below 2^-32 of the
+// maximum.  bf16 has fp32's range.
+template <typename T> constexpr float kLift = std::is_same<T, f16>::value ? 7.f : 0.f;
 
 template <int DP> struct Lds {
     static constexpr int CPR = DP / 8;                 // 16-byte chunks of a row
@@ -324,7 +329,7 @@ struct Rows {
             for (int d = 0; d < ND; d++) o[d] *= fix;
             m = mn;
         }
-        const float mu = m == -INFINITY ? 0.f : m;
+        const float mu = m == -INFINITY ? 0.f : m - kLift<T>;
         // (l takes a tile's weights at once: one by one those below half of its last
         // bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is)
         float sum = 0.f;
@@ -337,6 +342,12 @@ struct Rows {
                 pf[2 * n + e / 8][e % 8] = (T)w;
             }
         l += sum;
+    }
+    // After the last tile: l with both halves' keys, and m as what a weight of 1 stands
+    // for, by which parts are joined and lse is formed.
+    __device__ __forceinline__ void finish() {
+        l += __shfl_xor(l, 32);
+        m -= kLift<T>;
     }
     // This lane's part of a transposing read: dimensions 32 d .. 32 d + 31, keys 8 w
     // + 4 half .. + 3 of sixteen.
@@ -545,7 +556,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
         if (t + 1 < s.t1) step(t + 1, std::integral_constant<int, BUF>{});
     }
     if (!active) return;
-    w.l += __shfl_xor(w.l, 32);
+    w.finish();
 
     bool bad = false;
 #pragma unroll
@@ -661,7 +672,7 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDe
             step(t, std::integral_constant<int, 0>{});
             if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>{});
         }
-        w.l += __shfl_xor(w.l, 32);
+        w.finish();
     }
 
     // the waves' parts of the rows meet in LDS

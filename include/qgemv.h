@@ -456,7 +456,9 @@ qgemv_status qgemv_rope_append(const qgemv_kv_cache* cache, int64_t T, int in_ty
  * and lse = -inf.  Keys that a query does not see have no part in its result,
  * whatever their slots hold, infinities and NaN included.  Query head h reads
  * cache head h / (q_heads / heads).  Scores, m, l and sums are fp32; the
- * weights exp(x - m) are rounded to the cache's type for the matrix cores.
+ * weights exp(x - m) are rounded to the cache's type for the matrix cores (for
+ * fp16 scaled by 2^7 first, so that only what is below 2^-32 of a row's largest
+ * weight is lost).
  *   q: [T][ldq] of the cache's type, q_heads heads of head_dim; 16-byte rows.
  *   q_start: int32 [B + 1], kv_len: int32 [B]; starts are held to [0, T] and
  *      to their order.

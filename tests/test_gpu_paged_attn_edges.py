@@ -90,3 +90,14 @@ def test_a_long_flat_tail_beside_a_peak_counts_in_lse(qg, kind, Hq, gap):
     _, lse = Problem(qg, [(q, k, v)], kind).run()
     _, _, ref, tol = peaked_ref(q, k, v, kind)
     within(f64(lse)[0], np.full(Hq, ref), tol, "lse")
+
+
+@pytest.mark.parametrize("Hq", [1, 40])
+@pytest.mark.parametrize("gap", [16.8, 17.4, 18.5])
+def test_a_long_flat_tail_beside_a_peak_keeps_its_weight_in_fp16(qg, Hq, gap):
+    """131071 weights near 2^-25 of the largest, of which fp16's own range holds none or the first bit."""
+    say("attn tail", Hq, gap)
+    q, k, v = peaked("fp16", Hq, gap)
+    out, _ = Problem(qg, [(q, k, v)], "fp16").run()
+    ref, tol, _, _ = peaked_ref(q, k, v, "fp16")
+    within(f64(out)[0], np.tile(ref, (Hq, 1)), np.tile(tol, (Hq, 1)), "out")
