@@ -252,7 +252,7 @@ struct Rows {
     V8 qf[NS];
     f32x16 o[ND];
     float m, l;
-    float c2;                    // |scale| log2(e)
+    float c2;                    // what scores are multiplied by: |scale| log2(e)
     int p, z, p_lo, p_hi, z_hi;  // place and window start of this lane's row, and of the wave's rows
 
     // The rows first_row .. first_row + 31 of the block; this lane's is `row`.
@@ -264,8 +264,9 @@ struct Rows {
         p_lo = s.place(min(first_row / a.G, s.i1));
         p_hi = s.place(min((first_row + 31) / a.G, s.i1));
         z_hi = window_start(a, p_hi);
-        // (the sign of the scale is moved into q)
-        c2 = fabsf(a.scale) * 1.4426950408889634f;
+        // (the sign of the scale is moved into q, and so is a scale of 0: the -inf of a
+        // hidden key times 0 would be NaN)
+        c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const T* q = (const T*)a.q + (int64_t)(s.s0 + qi) * a.ldq + (int64_t)hq * a.D;
 #pragma unroll
         for (int k = 0; k < NS; k++) {
@@ -273,6 +274,7 @@ struct Rows {
             V8 f = {};
             if (d < a.D) f = *reinterpret_cast<const V8*>(q + d);
             if (a.scale < 0.f) f = -f;
+            if (a.scale == 0.f) f = f * (T)0.f;
             qf[k] = f;
         }
 #pragma unroll

@@ -1,4 +1,5 @@
-"""Attention over a paged cache: long rows of which one key holds almost all the weight."""
+"""Attention over a paged cache: long rows of which one key holds almost all the weight, and
+a scale of zero."""
 import numpy as np
 import pytest
 import torch
@@ -101,3 +102,47 @@ def test_a_long_flat_tail_beside_a_peak_keeps_its_weight_in_fp16(qg, Hq, gap):
     out, _ = Problem(qg, [(q, k, v)], "fp16").run()
     ref, tol, _, _ = peaked_ref(q, k, v, "fp16")
     within(f64(out)[0], np.tile(ref, (Hq, 1)), np.tile(tol, (Hq, 1)), "out")
+
+
+def median_us(f, n=5):
+    times = []
+    for _ in range(n + 1):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    return sorted(times[1:])[n // 2]
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("n", [1, 2048])
+def test_a_scale_of_zero_is_a_mean_and_takes_no_longer(qg, kind, n):
+    """All weights are 1, so the output is the mean of the values seen, and lse ln of their number."""
+    say("attn scale 0", kind, n)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    L, Hq, H, D = 2048, 8, 2, 128
+    q, k, v = (torch.randn(m, h, D, generator=g, device=DEV).to(TYPES[kind]) for m, h in ((n, Hq), (L, H), (L, H)))
+    p = Problem(qg, [(q, k, v)], kind, scale=0.0)
+    out, lse = p.run()
+    seen = np.arange(L - n + 1, L + 1)
+    sums, mass = (np.cumsum(t, 0)[L - n:] / seen[:, None, None] for t in (f64(v), np.abs(f64(v))))
+    ref = np.repeat(sums, Hq // H, 1)
+    within(f64(out), ref, rounded(np.repeat(mass, Hq // H, 1) * 2 * L * F32, ref, "fp32"), "out")
+    want = np.tile(np.log(seen)[:, None], (1, Hq))
+    within(f64(lse), want, (L + 16) * F32, "lse")
+    zero, p.scale = median_us(p.run), 0.1
+    assert median_us(p.run) > zero / 4   # (every row again by itself took tens of times as long)
+
+
+def test_a_scale_of_zero_keeps_what_is_not_finite(qg):
+    """0 * (q . k) is NaN where q or a seen key is not finite, and nothing where the key is not seen."""
+    say("attn scale 0 not finite")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    for n in (20, 70):
+        q, k, v = (torch.randn(n, 1, 64, generator=g, device=DEV).bfloat16() for _ in range(3))
+        k[9, 0, 3], q[4, 0, 7] = float("inf"), float("nan")
+        out, _ = Problem(qg, [(q, k, v)], "bf16", scale=0.0).run()
+        bad = torch.isnan(out[:, 0]).all(1).cpu().tolist()
+        assert bad == [i >= 9 or i == 4 for i in range(n)] and torch.isnan(out).any(2)[:, 0].cpu().tolist() == bad
