@@ -9,6 +9,8 @@
 // it, forms the rot_dim / 2 pairs once, in LDS.  Everything else is memory
 // traffic: each value is read once from memory and written once, 8 at a time.
 
+#include <algorithm>
+
 #include "qgemv_layer.h"
 
 namespace qgemv {
@@ -30,7 +32,8 @@ struct RopeDev {
     const int64_t* slots;
     const float* inv_freq;
     int64_t ldq, ldk, ldv, ldqo, page_stride, token_stride, head_stride, n_slots;
-    int T, q_heads, heads, D, rot, page_size, style;
+    int64_t first;  // the launch's first token
+    int q_heads, heads, D, rot, page_size, style;
     int items;  // chunks of a token
 };
 
@@ -38,7 +41,7 @@ template <typename TI, typename TO, RopeWalk WALK>
 __global__ __launch_bounds__(RWG) void k_rope_append(const RopeDev a) {
     __shared__ float2 cs[QGEMV_HEAD_DIM_MAX / 2];
     const int half = a.rot / 2;
-    const int64_t tok = blockIdx.x;
+    const int64_t tok = a.first + blockIdx.x;
     const int64_t slot = a.slots[tok];
     for (int f = threadIdx.x; f < half; f += RWG) {
         const double turns = (double)a.pos[tok] * (double)a.inv_freq[f] * 0.15915494309189535;
@@ -108,7 +111,7 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
     d.page_stride = a.c.page_stride; d.token_stride = a.c.token_stride;
     d.head_stride = a.c.head_stride;
     d.n_slots = (int64_t)a.c.n_pages * a.c.page_size;
-    d.T = a.T; d.q_heads = a.q_heads; d.heads = a.c.heads; d.D = a.c.head_dim; d.rot = a.rot_dim;
+    d.q_heads = a.q_heads; d.heads = a.c.heads; d.D = a.c.head_dim; d.rot = a.rot_dim;
     d.page_size = a.c.page_size; d.style = a.style;
     const RopeWalk walk = a.style == QGEMV_ROPE_HALVES ? (a.rot_dim % 16 == 0 ? kHalves : kSingle)
                                                        : (a.rot_dim % 8 == 0 ? kPairs : kSingle);
@@ -116,17 +119,23 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
     // few tokens: all of a token's chunks at once; many: one workgroup a token,
     // which forms its angles once
     const int rows = (d.items + RWG - 1) / RWG;
-    const dim3 grid((unsigned)a.T, (unsigned)(a.T <= 512 ? rows : 1));
+    // (a launch has fewer than 2^32 threads; what is past them would be left out
+    // without an error)
+    constexpr int kTokens = 1 << 23;
     with_type(a.in_type, [&](auto ti) {
         with_type16(a.c.type, [&](auto to) {
             using TI = decltype(ti);
             using TO = decltype(to);
-            if (walk == kHalves)
-                launch_kernel(k_rope_append<TI, TO, kHalves>, grid, dim3(RWG), 0, st, d);
-            else if (walk == kPairs)
-                launch_kernel(k_rope_append<TI, TO, kPairs>, grid, dim3(RWG), 0, st, d);
-            else
-                launch_kernel(k_rope_append<TI, TO, kSingle>, grid, dim3(RWG), 0, st, d);
+            for (d.first = 0; d.first < a.T; d.first += kTokens) {
+                const dim3 grid((unsigned)std::min<int64_t>(a.T - d.first, kTokens),
+                                (unsigned)(a.T <= 512 ? rows : 1));
+                if (walk == kHalves)
+                    launch_kernel(k_rope_append<TI, TO, kHalves>, grid, dim3(RWG), 0, st, d);
+                else if (walk == kPairs)
+                    launch_kernel(k_rope_append<TI, TO, kPairs>, grid, dim3(RWG), 0, st, d);
+                else
+                    launch_kernel(k_rope_append<TI, TO, kSingle>, grid, dim3(RWG), 0, st, d);
+            }
         });
     });
     return hipGetLastError();

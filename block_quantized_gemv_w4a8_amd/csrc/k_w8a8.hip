@@ -133,9 +133,14 @@ __global__ __launch_bounds__(64 * W) void k_quantize_rows(const T* __restrict__ 
 hipError_t launch_quantize_rows(const RowsArgs& a, hipStream_t st) {
     with_type(a.x_type, [&](auto t) {
         using T = decltype(t);
+        // (a launch has fewer than 2^32 threads; what is past them would be left out
+        // without an error)
+        constexpr int64_t kRows = 1 << 21;
         auto go = [&](auto w, auto ch) {
-            launch_kernel(k_quantize_rows<T, w, ch>, dim3((unsigned)a.M), dim3(64 * w), 0, st,
-                          (const T*)a.x, a.K, a.ldx, a.q, a.ldq, a.sx);
+            for (int64_t m = 0; m < a.M; m += kRows)
+                launch_kernel(k_quantize_rows<T, w, ch>, dim3((unsigned)std::min(a.M - m, kRows)),
+                              dim3(64 * w), 0, st, (const T*)a.x + m * a.ldx, a.K, a.ldx,
+                              a.q + m * a.ldq, a.ldq, a.sx + m);
         };
         // few rows: many threads a row; many rows: enough values a thread
         const bool many = a.M > 512;

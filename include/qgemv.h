@@ -415,8 +415,8 @@ enum { QGEMV_ROPE_HALVES = 0, QGEMV_ROPE_PAIRS = 1 };
  * p * page_stride + t * token_stride + h * head_stride + e of k and of v, so
  * slots-major and heads-major pools are both described.  k, v: 16-byte
  * aligned; strides: multiples of 8 elements; head_dim: a multiple of 8, at
- * most QGEMV_HEAD_DIM_MAX; page_size: any, at most 65536.  The structure is a
- * host structure, read during the call only. */
+ * most QGEMV_HEAD_DIM_MAX; page_size: any, at most 65536; heads: at most 65535.
+ * The structure is a host structure, read during the call only. */
 typedef struct {
     void* k;
     void* v;
@@ -438,7 +438,8 @@ typedef struct {
  *      token whose slot is negative or past the pool is not stored (its q is
  *      still written).  Slots of one call must differ.
  *   inv_freq: fp32 [rot_dim / 2] (NULL if rot_dim is 0); rot_dim even.
- *   q_out: [T][ldqo] of the cache's type, 16-byte aligned rows. */
+ *   q_out: [T][ldqo] of the cache's type, 16-byte aligned rows.
+ * Limits: T at most 2^28, q_heads at most 65535. */
 qgemv_status qgemv_rope_append(const qgemv_kv_cache* cache, int64_t T, int in_type,
                                const void* q, int64_t ldq, int q_heads, const void* k,
                                int64_t ldk, const void* v, int64_t ldv, const int32_t* pos,
@@ -471,7 +472,9 @@ qgemv_status qgemv_rope_append(const qgemv_kv_cache* cache, int64_t T, int in_ty
  *   out: [T][ldo] of out_type; rows of whole 16 bytes.  lse: fp32 [T][q_heads]
  *      or NULL.
  *   ws: ws_bytes of 16-byte aligned device memory for the parts of long rows
- *      (NULL with 0 for none), free again when the call's work is done. */
+ *      (NULL with 0 for none), free again when the call's work is done.
+ * Limits: T at most 2^28, B and q_heads at most 65535, max_q * q_heads at most
+ * 2^30, ldt at most 2^31 - 1. */
 qgemv_status qgemv_paged_attn(const qgemv_kv_cache* cache, const void* q, int64_t T, int64_t ldq,
                               int q_heads, const int32_t* q_start, const int32_t* kv_len, int B,
                               int max_q, int64_t max_kv, const int32_t* table, int64_t ldt,
@@ -486,13 +489,15 @@ qgemv_status qgemv_paged_attn(const qgemv_kv_cache* cache, const void* q, int64_
  * qgemv_quantize_act does per block.  x: x_type [M][ldx], K valid columns,
  * aligned to its elements; q: int8 [M][ldq], 16-byte aligned, ldq a multiple
  * of 16 and >= K; codes from K to the next multiple of 16 are written as zero.
- * sx: fp32 [M].  (Values are meant to be finite: an infinity makes the row's
- * scale infinite, and a NaN's code means nothing.) */
+ * sx: fp32 [M].  Limits: M and K at most 2^31 - 1.  (Values are meant to be
+ * finite: an infinity makes the row's scale infinite, and a NaN's code means
+ * nothing.) */
 qgemv_status qgemv_quantize_rows(const void* x, int x_type, int64_t M, int64_t K, int64_t ldx,
                                  int8_t* q, int64_t ldq, float* sx, qgemv_stream_t stream);
 
 /* y[m][n] = sx[m] * sw[n] * sum_k q[m][k] * w[n][k] (+ bias[n]), the sum exact
- * in int32, the rest fp32, rounded once to y_type; any M >= 0.
+ * in int32, the rest fp32, rounded once to y_type.  Limits: M and N at most
+ * 2^20, K at most QGEMV_W8A8_K_MAX.
  *   w: int8 [N][ldw], q: int8 [M][ldq]; 16-byte aligned, strides multiples of
  *      16 and >= K; what lies between K and a row's end is not used.
  *   sw, bias: fp32 [N] (bias may be NULL); sx: fp32 [M]; y: [M][ldy], aligned
