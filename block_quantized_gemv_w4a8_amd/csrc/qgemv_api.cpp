@@ -70,6 +70,10 @@ qgemv_status launched(hipError_t e, const char* what) {
     return QGEMV_OK;
 }
 
+// Whether workgroups of 256 with `threads` threads in all are one launch: from 2^32
+// threads on the runtime leaves some out without an error.
+bool one_launch(int64_t threads) { return (threads + 255) / 256 * 256 <= (int64_t)UINT32_MAX; }
+
 qgemv_status check_k(int64_t K) {
     if (K < 32 || K % 32 != 0)
         return fail(QGEMV_E_SHAPE, "K = %lld must be a positive multiple of 32", (long long)K);
@@ -312,7 +316,7 @@ qgemv_status qgemv_quantize_act(const float* x, int64_t M, int64_t K, int64_t ld
     if (M > (int64_t)1 << 31 || ldx > (int64_t)1 << 40 || K > (int64_t)1 << 31)
         return fail(QGEMV_E_UNSUPPORTED, "qgemv_quantize_act: sizes beyond this library's range");
     const int64_t Kp = (K + 255) / 256 * 256;
-    if (M * (Kp / 32) * 8 / 256 >= ((int64_t)1 << 31))
+    if (!one_launch(M * (Kp / 32) * 8))
         return fail(QGEMV_E_UNSUPPORTED, "qgemv_quantize_act: M*K too large for one launch");
     if (!aligned(x, 4)) return fail(QGEMV_E_ALIGN, "qgemv_quantize_act: x must be 4-byte aligned");
     if ((st = check_act_align(q, d, s)) != QGEMV_OK) return st;
@@ -511,7 +515,9 @@ qgemv_status qgemv_block_dots(int fmt, const void* w, int64_t N, int64_t K, int6
     if (fmt < QGEMV_FMT_Q4_0 || fmt > QGEMV_FMT_Q6_K_R8)
         return fail(QGEMV_E_UNSUPPORTED, "%s: unknown format %d", name, fmt);
     if (K > QGEMV_K_MAX) return fail(QGEMV_E_UNSUPPORTED, "%s: K exceeds QGEMV_K_MAX", name);
-    if (nrows * ((K + 255) / 64) / 256 >= ((int64_t)1 << 31))
+    const bool per32 = fmt == QGEMV_FMT_Q4_0 || fmt == QGEMV_FMT_Q8_0;   // rows of K/32 blocks
+    if (nrows > (int64_t)UINT32_MAX ||
+        !one_launch(nrows * (per32 ? (K + 63) / 64 : (K + 255) / 256 * 4)))
         return fail(QGEMV_E_UNSUPPORTED, "%s: too many rows for one launch", name);
     if (!aligned(w, 16)) return fail(QGEMV_E_ALIGN, "%s: w must be 16-byte aligned", name);
     if (!aligned(q, 16)) return fail(QGEMV_E_ALIGN, "%s: q must be 16-byte aligned", name);
@@ -537,13 +543,13 @@ qgemv_status qgemv_block_dots_staged(int fmt, const void* w, int64_t N, int64_t 
     if (fmt < QGEMV_FMT_Q4_0 || fmt > QGEMV_FMT_Q6_K_R8)
         return fail(QGEMV_E_UNSUPPORTED, "%s: unknown format %d", name, fmt);
     if (K > QGEMV_K_MAX) return fail(QGEMV_E_UNSUPPORTED, "%s: K exceeds QGEMV_K_MAX", name);
-    if (nrows * 4 >= ((int64_t)1 << 31))
-        return fail(QGEMV_E_UNSUPPORTED, "%s: too many rows for one launch", name);
     if (!qgemv::block_dots_staged_supported(fmt, K, wk))
         return fail(QGEMV_E_UNSUPPORTED,
                     "%s: split-K width %d with K = %lld has no staged configuration (wk in "
                     "1, 2, 4; at most 128 units per slice)",
                     name, wk, (long long)K);
+    if (nrows > (int64_t)UINT32_MAX || !one_launch(nrows * wk * 64))
+        return fail(QGEMV_E_UNSUPPORTED, "%s: too many rows for one launch", name);
     if (!aligned(w, 16)) return fail(QGEMV_E_ALIGN, "%s: w must be 16-byte aligned", name);
     if ((st = check_act_align(q, d, s)) != QGEMV_OK) return st;
     if (!aligned(dots, 4)) return fail(QGEMV_E_ALIGN, "%s: dots must be 4-byte aligned", name);

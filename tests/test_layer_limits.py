@@ -5,7 +5,7 @@ import torch
 
 import block_quantized_gemv_w4a8_amd as qg
 from gpu_util import DEV, say
-from test_layer_gates import BASE, cache, status
+from test_layer_gates import A, BASE, cache, status
 
 WIDE = dict(head_dim=8, head_stride=8, token_stride=8 * 65535, page_stride=0, n_pages=1)
 PAST = [
@@ -52,6 +52,24 @@ def test_sizes_past_the_limits_are_refused(name, kw):
 @pytest.mark.parametrize("name,kw", WITHIN)
 def test_sizes_at_the_limits_reach_the_device(name, kw):
     assert call(name, kw) == qg.QGEMV_E_DEVICE, qg.qgemv_last_error()
+
+
+@pytest.mark.parametrize("name,most,args", [
+    # 64 threads a row of up to 256 values
+    ("qgemv_quantize_act", (1 << 26) - 4, lambda n: (A, n, 32, 32, A, A, A, None)),
+    # a thread for each 64 weights, of which Q4_0 rows have K / 64 and Q4_K rows a multiple of four
+    ("qgemv_block_dots", (1 << 32) - 256, lambda n: (qg.QGEMV_FMT_Q4_0, A, n, 32, 0, n, A, A, None)),
+    ("qgemv_block_dots", (1 << 30) - 64, lambda n: (qg.QGEMV_FMT_Q4_K, A, n, 32, 0, n, A, A, None)),
+    # a wave for each slice of a row
+    ("qgemv_block_dots_staged", (1 << 25) - 2, lambda n: (qg.QGEMV_FMT_Q4_K, A, n, 4096, 0, n, A, A, A, 2, A, None)),
+])
+def test_one_launch_has_fewer_than_2_to_32_threads(name, most, args):
+    """What is past them the runtime would leave out without an error."""
+    f = getattr(qg._lib, name)
+    assert f(*args(most + 1)) == qg.QGEMV_E_UNSUPPORTED, qg.qgemv_last_error()
+    assert "one launch" in qg.qgemv_last_error()
+    if torch.cuda.device_count() == 0:
+        assert f(*args(most)) == qg.QGEMV_E_DEVICE
 
 
 @pytest.mark.gpu
