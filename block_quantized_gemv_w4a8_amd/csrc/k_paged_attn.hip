@@ -254,6 +254,7 @@ struct Rows {
     float m, l;
     float c2;                    // what scores are multiplied by: |scale| log2(e)
     int p, z, p_lo, p_hi, z_hi;  // place and window start of this lane's row, and of the wave's rows
+                                 // (p_lo: below every key for a scale of 0, so that hide has every tile)
 
     // The rows first_row .. first_row + 31 of the block; this lane's is `row`.
     __device__ __forceinline__ void start(const AttnDev& a, const Span& s, int h, int row, int first_row) {
@@ -261,11 +262,11 @@ struct Rows {
         const int qi = row / a.G, hq = h * a.G + row - qi * a.G;
         p = s.place(qi);
         z = window_start(a, p);
-        p_lo = s.place(min(first_row / a.G, s.i1));
+        p_lo = a.scale == 0.f ? INT32_MIN : s.place(min(first_row / a.G, s.i1));
         p_hi = s.place(min((first_row + 31) / a.G, s.i1));
         z_hi = window_start(a, p_hi);
-        // (the sign of the scale is moved into q, and so is a scale of 0: the -inf of a
-        // hidden key times 0 would be NaN)
+        // (the sign of the scale is moved into q; a scale of 0 is taken in hide, because
+        // the -inf of a hidden key times 0 would be NaN)
         c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const T* q = (const T*)a.q + (int64_t)(s.s0 + qi) * a.ldq + (int64_t)hq * a.D;
 #pragma unroll
@@ -274,7 +275,6 @@ struct Rows {
             V8 f = {};
             if (d < a.D) f = *reinterpret_cast<const V8*>(q + d);
             if (a.scale < 0.f) f = -f;
-            if (a.scale == 0.f) f = f * (T)0.f;
             qf[k] = f;
         }
 #pragma unroll
@@ -303,6 +303,10 @@ struct Rows {
     __device__ __forceinline__ void hide(const AttnDev& a, int j0, unsigned long long there, f32x16 (&x)[NX]) {
         const unsigned long long full = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
         if ((there & full) == full && j0 + KT - 1 <= p_lo && (j0 >= z_hi || j0 + KT - 1 < a.sinks)) return;
+        if (a.scale == 0.f) {
+#pragma unroll
+            for (int n = 0; n < NX; n++) x[n] *= 0.f;
+        }
         const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
         // the keys that this lane's row sees, from the first that the lane has on
         const int half = (threadIdx.x & 63) >> 5;
