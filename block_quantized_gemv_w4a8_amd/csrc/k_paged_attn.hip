@@ -786,7 +786,7 @@ static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, i
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);
     int64_t seen = max_kv;
     if (d.window > 0)
-        seen = std::min(seen, (int64_t)d.window + rows / d.G + std::min(d.sinks, d.window) + 2 * kt);
+        seen = std::min(seen, (int64_t)d.window + rows / d.G + d.sinks + 2 * kt);
     const int64_t tiles = std::max<int64_t>(1, (seen + kt - 1) / kt);
     const int64_t blocks = (int64_t)d.row_tiles * d.heads * d.B;
     const int64_t per = (int64_t)d.T * d.q_heads * (d.D + 2) * 4;

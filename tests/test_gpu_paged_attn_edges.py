@@ -1,11 +1,11 @@
-"""Attention over a paged cache: long rows of which one key holds almost all the weight, and
-a scale of zero."""
+"""Attention over a paged cache: long rows of which one key holds almost all the weight,
+a scale of zero, and how long rows are split."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import DEV, say
-from layer_ref import F32, HALF, TYPES, f64, rounded, within
+from layer_ref import F32, HALF, TYPES, attend, f64, rounded, within
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
@@ -146,3 +146,35 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(qg):
         out, _ = Problem(qg, [(q, k, v)], "bf16", scale=0.0).run()
         bad = torch.isnan(out[:, 0]).all(1).cpu().tolist()
         assert bad == [i >= 9 or i == 4 for i in range(n)] and torch.isnan(out).any(2)[:, 0].cpu().tolist() == bad
+
+
+def check(p, seqs):
+    """The problem's outputs against the 64-bit form."""
+    at = 0
+    for b, (q, k, v) in enumerate(seqs):
+        n, L = len(q), len(k)
+        o, tol, l, tl = attend(f64(q), f64(k), f64(v), np.arange(L - n, L), p.window, p.sinks, p.scale, p.kind, "fp32")
+        within(f64(p.out)[at:at + n].reshape(o.shape), o, tol, f"out of sequence {b}")
+        within(f64(p.lse)[at:at + n], l, tl, f"lse of sequence {b}")
+        at += n
+
+
+def parts_written(p):
+    """How many parts of a row a call left in its workspace; its outputs are those of the call."""
+    ws = torch.full((p.qg.QGEMV_WS_BYTES // 4,), float("nan"), device=DEV)
+    p.run(ws, p.qg.QGEMV_WS_BYTES)
+    return int((~torch.isnan(ws)).sum()) / (p.Hq * (p.D + 2))
+
+
+def normal(g, *shape, kind="bf16"):
+    return torch.randn(*shape, generator=g, device=DEV).to(TYPES[kind])
+
+
+def test_more_sinks_than_the_window_count_in_the_split(qg):
+    """One token that sees 4096 sinks and 64 keys of its window: 130 tiles of 32."""
+    say("attn sinks above the window")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    seqs = [(normal(g, 1, 8, 64), normal(g, 8192, 2, 64), normal(g, 8192, 2, 64))]
+    p = Problem(qg, seqs, "bf16", window=64, sinks=4096, scale=0.125)
+    assert parts_written(p) >= 4
+    check(p, seqs)
