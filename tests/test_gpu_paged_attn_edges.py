@@ -1,5 +1,5 @@
 """Attention over a paged cache: long rows of which one key holds almost all the weight,
-a scale of zero, and how long rows are split."""
+a scale of zero, how long rows are split, and the workspace that this takes."""
 import numpy as np
 import pytest
 import torch
@@ -190,3 +190,65 @@ def test_one_long_sequence_among_short_ones_is_split(qg, n):
     p = Problem(qg, seqs, "bf16", scale=0.3)
     assert parts_written(p) >= 4 * n
     check(p, seqs)
+
+
+SPLIT = {"single tokens": (1, (5000, 700, 9000)), "chunks": (40, (3000, 40, 2500))}
+
+
+def split_problem(qg, name, kind="fp16", seed=3):
+    n, lengths = SPLIT[name]
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    seqs = [(normal(g, n, 4, 64, kind=kind), normal(g, L, 2, 64, kind=kind), normal(g, L, 2, 64, kind=kind)) for L in lengths]
+    return Problem(qg, seqs, kind, scale=0.125), seqs
+
+
+@pytest.mark.parametrize("name", SPLIT)
+def test_a_workspace_of_any_size_is_enough_and_is_not_passed(qg, name):
+    """From none to one part more than the call takes, a part of a row at a time, and sizes
+    beside those: results are right, and nothing is written past ws_bytes."""
+    p, seqs = split_problem(qg, name)
+    wanted = int(parts_written(p) / p.max_q)
+    assert wanted >= 3
+    sizes = {0, 16, p.part - 16, p.part, p.part + 16}
+    for parts in range(2, 12):
+        sizes |= {parts * p.part - 16, parts * p.part, parts * p.part + 48}
+    used = []
+    for size in sorted(sizes):
+        say("attn workspace", name, size)
+        ws = torch.full((size // 4 + 4096,), float("nan"), device=DEV)
+        p.out.fill_(7)
+        p.run(ws if size else None, size)
+        torch.cuda.synchronize()
+        check(p, seqs)
+        assert torch.isnan(ws[size // 4:]).all()
+        used.append(int((~torch.isnan(ws)).sum()))
+    # (fewer than two parts are none)
+    assert used[0] == 0 and used == sorted(used) and used[-1] >= 3 * p.max_q * p.Hq * (p.D + 2)
+
+
+@pytest.mark.parametrize("name", SPLIT)
+def test_a_captured_split_call_replays(qg, name):
+    """Both launches of a call in one graph: every replay on new values is the eager call bit
+    for bit, with eager work between."""
+    p, _ = split_problem(qg, name)
+    ws = torch.empty(qg.QGEMV_WS_BYTES // 4, device=DEV)
+    assert parts_written(p) >= 3 * p.max_q
+    p.run(ws, qg.QGEMV_WS_BYTES)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run(ws, qg.QGEMV_WS_BYTES)
+    for i in range(4):
+        say("attn split replay", name, i)
+        other, seqs = split_problem(qg, name, seed=10 + i)
+        for mine, new in zip([p.q, *p.pools], [other.q, *other.pools]):
+            mine.copy_(new)
+        p.out.fill_(7)
+        ws.fill_(float("nan"))
+        graph.replay()
+        got = p.out.clone(), p.lse.clone()
+        torch.cuda.synchronize()
+        check(p, seqs)
+        p.run(ws, qg.QGEMV_WS_BYTES)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], p.out) and torch.equal(got[1], p.lse)
