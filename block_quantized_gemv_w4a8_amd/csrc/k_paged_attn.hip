@@ -780,12 +780,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 // 4096 over six sequences: five parts 25 us, sixteen 43; nine sequences of chunks:
 // one part 51 us, two 96).  Long lists go on to `long_slots` in parts of four times
 // as many tiles, where a CU holds that many workgroups (64 dimensions: 2449
-// queries over 3695 keys, 14 heads on 2, one part 74.7 us, three 61.8).  max_kv may be
-// the length of one sequence among many short ones: parts of sixteen times as many
-// tiles are taken as if that one had the device to itself (32 heads on 8 of 128, one
-// sequence of 131072 keys among 32 of 500: one part 1352 us, sixteen 156; 64 of
-// 8192, of which none is split so, 362 us, with parts of half as many tiles 374, of
-// a quarter 384).
+// queries over 3695 keys, 14 heads on 2, one part 74.7 us, three 61.8).
 static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int long_slots,
                   int64_t ws_bytes, void* ws) {
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);
@@ -797,7 +792,6 @@ static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, i
     const int64_t per = (int64_t)d.T * d.q_heads * (d.D + 2) * 4;
     int64_t splits = std::max(std::min(slots / blocks, (tiles + min_tiles - 1) / min_tiles),
                               std::min(long_slots / blocks, tiles / (4 * min_tiles)));
-    splits = std::max(splits, std::min(slots / ((int64_t)d.row_tiles * d.heads), tiles / (16 * min_tiles)));
     splits = std::max<int64_t>(1, std::min(splits, std::min<int64_t>(ws_bytes, QGEMV_WS_BYTES) / per));
     d.splits = (int)splits;
     d.split_tiles = (int)((tiles + splits - 1) / splits);

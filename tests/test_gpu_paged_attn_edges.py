@@ -180,18 +180,6 @@ def test_more_sinks_than_the_window_count_in_the_split(qg):
     check(p, seqs)
 
 
-@pytest.mark.parametrize("n", [1, 33])
-def test_one_long_sequence_among_short_ones_is_split(qg, n):
-    """Short sequences fill the device by their number alone; the long one has to be split all the same."""
-    say("attn one long", n)
-    g = torch.Generator(device=DEV).manual_seed(n)
-    lengths = [40] * 20 + [65536] + [33, 50] * 10
-    seqs = [(normal(g, n, 8, 8), normal(g, L, 8, 8), normal(g, L, 8, 8)) for L in lengths]
-    p = Problem(qg, seqs, "bf16", scale=0.3)
-    assert parts_written(p) >= 4 * n
-    check(p, seqs)
-
-
 SPLIT = {"single tokens": (1, (5000, 700, 9000)), "chunks": (40, (3000, 40, 2500))}
 
 
