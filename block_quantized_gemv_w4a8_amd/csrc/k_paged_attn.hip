@@ -1,7 +1,8 @@
 // k_paged_attn.hip -- attention over a paged cache with causal order, an
 // optional sliding window and the first keys that stay visible.
 //
-// One pass over the keys with the running maximum m and sum l of a softmax:
+// One pass over the keys with the running maximum m and sum l of a softmax
+// (Milakov and Gimelshein, "Online normalizer calculation for softmax", 2018):
 // for each tile of keys, where max x exceeds m, o and l are scaled by
 // exp(m - m') and m becomes m'; then exp(x - m) v and exp(x - m) are added.
 //
@@ -487,14 +488,15 @@ struct Pages {
 };
 
 // Many rows: NW waves of 32 rows each, which share every tile of KT keys, the next
-// tile on its way while one is used.  A row's 32 weights of a tile cost a lane's
-// vector pipe about what its matrix instructions cost the matrix pipe (206 and 32
-// instructions a tile of 64 keys at 128 dimensions), and waves of two workgroups
-// a SIMD share the two: 8192 tokens of 32 heads on 8, causal, take 567 us, 970
-// TFLOP/s.  (With the LDS places formed for each read, 302 vector instructions,
-// it took 629; with the scores of 32 keys formed beside the weights of the 32
-// before, 660.)  Batches of short chunks are bound by the tiles' chain of loads,
-// scores and weights: 43 us for nine sequences with a window of 1024.
+// tile on its way while one is used, and waited for whole.  Bound by a tile's chain
+// of loads, scores, weights and products, about 2.2 us at 64 dimensions as at 128
+// with two workgroups a CU: the vector and the matrix pipe have about the same work
+// (206 and 32 instructions a wave and tile of 64 keys at 128 dimensions) but hardly
+// have it at once, the matrix cores being busy 0.47 of the time.  8192 tokens of 32
+// heads on 8, causal, take 560 to 600 us with the machine, 920 to 980 TFLOP/s (with
+// the LDS places formed for each read, 302 vector instructions, 629 where this took
+// 567; with the scores of 32 keys formed beside the weights of the 32 before, 660);
+// nine sequences of chunks with a window of 1024 43 us.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
     typedef Rows<T, DP, KT> R;
@@ -610,8 +612,9 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
 // K and two V tiles; a tile's K makes room for the K after next as soon as the
 // scores are formed, and V likewise, so that three of the four are always on
 // their way.  Bound by the cache's bytes: 64 sequences of up to 8192 keys take 313
-// us, 5.5 TB/s (361 with whole tiles in turn, two to a wave); one short sequence
-// is bound by the chain of lengths, pages, keys, 9.6 us.
+// us, 5.5 TB/s (361 with whole tiles in turn, two to a wave; 256 dimensions, two
+// waves a CU, 4.8 TB/s); one short sequence is bound by the chain of lengths, pages,
+// keys, 9.6 us.
 template <typename T, typename TO, int DP, int NW>
 __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn_few(const AttnDev a) {
     constexpr int KT = 32, ROWS = 32;
@@ -774,13 +777,20 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 }
 
 // How many parts the longest list of tiles is split into: as many as fill the
-// device once (`slots` workgroups), of at least min_tiles each (four tiles of the
-// many-row kernel: 2 x 178 queries over 2107 keys, one cache head, 24.7 us with
-// eight, 22.1 with four).  More parts than that only cost the join (a window of
-// 4096 over six sequences: five parts 25 us, sixteen 43; nine sequences of chunks:
-// one part 51 us, two 96).  Long lists go on to `long_slots` in parts of four times
-// as many tiles, where a CU holds that many workgroups (64 dimensions: 2449
-// queries over 3695 keys, 14 heads on 2, one part 74.7 us, three 61.8).
+// How many parts the longest list of tiles is split into: as many as fill the
+// device once (`slots` workgroups), of at least min_tiles each.  (Four tiles of the
+// many-row kernel: over 36 sizes 4% above the best of each on average, two 8%, eight
+// 6%, sixteen 10%; four a wave of the other: 4%, two 3%, eight 10%.)  More parts
+// than that only cost the join (a window of 4096 over six sequences: five parts 25
+// us, sixteen 43; nine sequences of chunks: one part 51 us, two 96).  Long lists of
+// 64 dimensions, where a CU holds four workgroups, go on to `long_slots` in parts of
+// four times as many tiles: over 14 sizes of 300 to 4096 queries 0.73 to 1.03 of the
+// time (4 x 300 queries over 8192 keys, 16 heads, 102 us to 74), where 128
+// dimensions took 0.78 to 1.40.  All sequences are taken to be as long as max_kv: one
+// of 131072 keys among 32 of 500 (32 heads on 8 of 128) stays whole, 1350 us.  More
+// parts on the chance of that, sixteen, take it in 133 us, but 64 of 500 with a max_kv
+// of 131072 in 103 where this takes 30: workgroups without work hold a CU's LDS while
+// they find out.
 static void split(AttnDev& d, int64_t max_kv, int rows, int kt, int min_tiles, int slots, int long_slots,
                   int64_t ws_bytes, void* ws) {
     d.row_tiles = (int)(((int64_t)d.max_q * d.G + rows - 1) / rows);

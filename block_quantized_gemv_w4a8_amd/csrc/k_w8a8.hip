@@ -194,9 +194,9 @@ __device__ __forceinline__ i32x4 codes16(const int8_t* row, int64_t k, int64_t K
 // where runs take 33: 3539 x 7187 x 306).
 //
 // Large tiles are bound by the matrix cores at the clock that their power leaves:
-// 4096 x 28672 x 4096 takes 465 us, 2070 TOP/s (2110 is what the library's int8
-// product reaches, its sums unscaled); the matrix instructions alone, on the same
-// codes, run at 2870, and codes of zero at 2450.  Small ones are bound by the way
+// 4096 x 28672 x 4096 takes 470 us, 2050 TOP/s (2110 to 2150 is what the library's
+// int8 product reaches, its sums unscaled); the matrix instructions alone, on the
+// same codes, run at 2870, and codes of zero at 2450.  Small ones are bound by the way
 // from memory to LDS, so they have more stages on their way: 64 x 4096 x 14336
 // with a ring of two 35 us, of four 20.
 template <int BM, int BN, int WM, int WN, int RING>
@@ -593,8 +593,8 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 8 : 5) void k_w8a8_stream(con
 // At most kTokenM rows, from x with their quantisation in the launch or (TX is
 // int8_t) from their codes: every workgroup forms the codes in its LDS (the
 // first one also writes them out) while its first weight codes are on their
-// way.  Otherwise as k_w8a8_stream.  1 x 28672 x 4096 takes 22.2 us from codes,
-// 5.3 TB/s, and 23.8 from x.
+// way.  Otherwise as k_w8a8_stream.  1 x 28672 x 4096 takes 23.0 us from codes,
+// 5.1 TB/s, and 24.7 from x in the same run.
 constexpr int kTokenM = 2;
 
 template <typename TX, typename TY, int WAVES, int U>

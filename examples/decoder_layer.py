@@ -3,7 +3,7 @@ then single tokens of a ragged batch.
 
     python examples/decoder_layer.py
 
-A layer's step is five calls of the library: the q|k|v product (the activation
+A layer's step is six calls of the library: the q|k|v product (the activation
 quantised in the call), rope-and-append, attention over the cache, the output
 product, and the two products of the feed-forward part; norms, the gate and
 residual sums are torch's.  The same calls serve chunks of prompts and single

@@ -461,11 +461,12 @@ qgemv_status qgemv_rope_append(const qgemv_kv_cache* cache, int64_t T, int in_ty
  * fp16 scaled by 2^7 first, so that only what is below 2^-32 of a row's largest
  * weight is lost).
  *   q: [T][ldq] of the cache's type, q_heads heads of head_dim; 16-byte rows.
- *   q_start: int32 [B + 1], kv_len: int32 [B]; starts are held to [0, T] and
- *      to their order.
+ *   q_start: int32 [B + 1], kv_len: int32 [B]; starts are held to [0, T], and
+ *      a sequence that ends before it starts has no queries.  (Starts that fall
+ *      can so give a row to two sequences; it then holds either's result.)
  *   max_q: at least the most queries of a sequence (rows past it are not
  *      written); max_kv: the longest kv_len expected, used only to choose how
- *      the work is split.
+ *      the work is split (the nearer to what the sequences have, the better).
  *   table: int32 [B][ldt]; a page number outside the pool, or a page past
  *      column ldt, means that its keys are absent: they are seen by no query.
  *      Pages that no query sees may so be given back and marked -1.
@@ -483,8 +484,8 @@ qgemv_status qgemv_paged_attn(const qgemv_kv_cache* cache, const void* q, int64_
                               qgemv_stream_t stream);
 
 /* Row quantisation to int8 with one scale per row (token of an activation, or
- * output channel of a weight): amax = max|x_k| over the row; amax == 0 -> scale
- * 0 and codes 0; otherwise sx = amax / 127 (IEEE fp32 division) and q_k =
+ * output channel of a weight): amax = max|x_k| over the row, sx = amax / 127
+ * (IEEE fp32 division); sx == 0 -> codes 0; otherwise q_k =
  * clamp(round_half_away(x_k / sx), -127, 127) (IEEE division), as
  * qgemv_quantize_act does per block.  x: x_type [M][ldx], K valid columns,
  * aligned to its elements; q: int8 [M][ldq], 16-byte aligned, ldq a multiple
