@@ -56,6 +56,7 @@ EXPORTS = [
     "qgemv_block_dots", "qgemv_block_dots_staged", "qgemm_small_m_block_dots",
     "qgemv_rope_append", "qgemv_paged_attn", "qgemv_quantize_rows", "qgemm_w8a8",
     "qgemm_quantize_w8a8",
+    "qgemv_rope_append_q8", "qgemv_paged_attn_q8", "qgemv_cache_read_q8", "qgemv_verify_draft",
 ]
 
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -388,6 +389,81 @@ def qgemm_quantize_w8a8(w, ldw, sw, N, K, M, x, x_type, ldx, q, ldq, sx, bias, y
                                            _ptr(q), ldq, _ptr(sx), _ptr(bias), _ptr(y), y_type,
                                            ldy, _ptr(ws), ws_bytes, _stream(stream)),
                   "qgemm_quantize_w8a8")
+
+
+class KvCacheQ8(ctypes.Structure):
+    """qgemv_kv_cache_q8 of the header; kv_cache_q8() fills one from torch tensors."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", _I64),
+                ("token_stride", _I64), ("head_stride", _I64), ("scale_page_stride", _I64),
+                ("scale_token_stride", _I64), ("scale_head_stride", _I64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+_KV8 = ctypes.POINTER(KvCacheQ8)
+_lib.qgemv_rope_append_q8.restype = _I
+_lib.qgemv_rope_append_q8.argtypes = [_KV8, _I64, _I, _P, _I64, _I, _P, _I64, _P, _I64, _P, _P, _P,
+                                      _I, _I, _P, _I, _I64, _P]
+_lib.qgemv_paged_attn_q8.restype = _I
+_lib.qgemv_paged_attn_q8.argtypes = [_KV8, _P, _I, _I64, _I64, _I, _P, _P, _I, _I, _I64, _P, _I64,
+                                     _F, _I, _I, _P, _I, _I64, _P, _P, _I64, _P]
+_lib.qgemv_cache_read_q8.restype = _I
+_lib.qgemv_cache_read_q8.argtypes = [_KV8, _I64, _P, _P, _I64, _P, _I64, _I, _P]
+_lib.qgemv_verify_draft.restype = _I
+_lib.qgemv_verify_draft.argtypes = [_P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P, _I64, _P, _P, _P,
+                                    _P, _P, _I64, _P]
+
+
+def kv_cache_q8(k, v, k_scale, v_scale) -> KvCacheQ8:
+    """Descriptor of an 8-bit cache: int8 pools k and v [pages, page_size, heads, head_dim] of one
+    set of strides, and fp32 scales k_scale and v_scale [pages, page_size, heads] of one set (a
+    heads-major pool is passed as its transposed view).  It holds addresses only: the pools and
+    scales must outlive it."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != torch.int8 or v.dtype != torch.int8:
+        raise ValueError("k and v must be 4-D int8 tensors of one shape")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v must have the same strides, with head_dim contiguous")
+    if k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or \
+            k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or \
+            k_scale.stride() != v_scale.stride():
+        raise ValueError("k_scale and v_scale must be fp32 tensors of the pools' first three sizes, "
+                         "with the same strides")
+    if len({t.device for t in (k, v, k_scale, v_scale)}) != 1:
+        raise ValueError("k, v, k_scale and v_scale must be on one device")
+    return KvCacheQ8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     *k.stride()[:3], *k_scale.stride(), *k.shape)
+
+
+def qgemv_rope_append_q8(cache, T, in_type, q, ldq, q_heads, k, ldk, v, ldv, pos, slots, inv_freq,
+                         rot_dim, style, q_out, q_type, ldqo, stream=None):
+    return _check(_lib.qgemv_rope_append_q8(cache, T, in_type, _ptr(q), ldq, q_heads, _ptr(k), ldk,
+                                            _ptr(v), ldv, _ptr(pos), _ptr(slots), _ptr(inv_freq),
+                                            rot_dim, style, _ptr(q_out), q_type, ldqo,
+                                            _stream(stream)), "qgemv_rope_append_q8")
+
+
+def qgemv_paged_attn_q8(cache, q, q_type, T, ldq, q_heads, q_start, kv_len, B, max_q, max_kv, table,
+                        ldt, scale, window, sinks, out, out_type, ldo, lse=None, ws=None,
+                        ws_bytes=0, stream=None):
+    return _check(_lib.qgemv_paged_attn_q8(cache, _ptr(q), q_type, T, ldq, q_heads, _ptr(q_start),
+                                           _ptr(kv_len), B, max_q, max_kv, _ptr(table), ldt, scale,
+                                           window, sinks, _ptr(out), out_type, ldo, _ptr(lse),
+                                           _ptr(ws), ws_bytes, _stream(stream)),
+                  "qgemv_paged_attn_q8")
+
+
+def qgemv_cache_read_q8(cache, T, slots, k_out, ldk, v_out, ldv, out_type, stream=None):
+    return _check(_lib.qgemv_cache_read_q8(cache, T, _ptr(slots), _ptr(k_out), ldk, _ptr(v_out),
+                                           ldv, out_type, _stream(stream)), "qgemv_cache_read_q8")
+
+
+def qgemv_verify_draft(logits, logits_type, T, V, ldl, q_start, B, max_q, tokens, draft, ldd, u,
+                       temperature, accepted, next, ws=None, ws_bytes=0, stream=None):
+    return _check(_lib.qgemv_verify_draft(_ptr(logits), logits_type, T, V, ldl, _ptr(q_start), B,
+                                          max_q, _ptr(tokens), _ptr(draft), ldd, _ptr(u),
+                                          _ptr(temperature), _ptr(accepted), _ptr(next), _ptr(ws),
+                                          ws_bytes, _stream(stream)), "qgemv_verify_draft")
 
 
 GEMV = {"q4_0": qgemv_q4_0, "q4_k": qgemv_q4_k, "q6_k": qgemv_q6_k, "q8_0": qgemv_q8_0,

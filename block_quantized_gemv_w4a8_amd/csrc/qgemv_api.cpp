@@ -275,7 +275,8 @@ const char* qgemv_build_info(void) {
            "block_dots=lds-rows,staged-stream,small_m_mfma_tiles "
            "fused=q4_k_swiglu_quantize,quantize_gemv,quantize_q4_k_swiglu multi=multi,quantize_multi(<=8) "
            "stream_read=calibration K_max=32768 M_max=64 "
-           "layer=rope_append,paged_attn(mfma_32x32x16),quantize_rows,w8a8(mfma_i8_32x32x32,16x16x64)";
+           "layer=rope_append,paged_attn(mfma_32x32x16),quantize_rows,w8a8(mfma_i8_32x32x32,16x16x64) "
+           "cache8=rope_append_q8,paged_attn_q8(mfma_32x32x16_f16),cache_read_q8 verify_draft(fp64 sums)";
 }
 
 const char* qgemv_last_error(void) { return g_last_error; }
@@ -562,3 +563,4 @@ qgemv_status qgemv_block_dots_staged(int fmt, const void* w, int64_t N, int64_t 
 }  // extern "C"
 
 #include "qgemv_layer_api.h"
+#include "qgemv_cache8_api.h"

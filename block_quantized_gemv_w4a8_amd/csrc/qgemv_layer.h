@@ -129,4 +129,74 @@ struct W8A8Args {
 hipError_t launch_w8a8(const W8A8Args& a, hipStream_t st);
 hipError_t launch_quantize_w8a8(const RowsArgs& r, const W8A8Args& a, hipStream_t st);
 
+// ---- the 8-bit cache and the verification of drafted tokens
+struct Rope8Args {
+    qgemv_kv_cache_q8 c;
+    int T;
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    int in_type, q_heads;
+    const int32_t* pos;
+    const int64_t* slots;
+    const float* inv_freq;
+    int rot_dim, style;
+    void* q_out;
+    int q_type;
+    int64_t ldqo;
+};
+hipError_t launch_rope_append_q8(const Rope8Args& a, hipStream_t st);
+
+struct Attn8Args {
+    qgemv_kv_cache_q8 c;
+    const void* q;
+    int q_type, T;
+    int64_t ldq;
+    int q_heads;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    int B, max_q;
+    int64_t max_kv;
+    const int32_t* table;
+    int64_t ldt;
+    float scale;
+    int window, sinks;
+    void* out;
+    int out_type;
+    int64_t ldo;
+    float* lse;
+    void* ws;
+    int64_t ws_bytes;
+};
+hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st);
+
+struct Read8Args {
+    qgemv_kv_cache_q8 c;
+    int64_t T;
+    const int64_t* slots;
+    void* k_out;
+    int64_t ldk;
+    void* v_out;
+    int64_t ldv;
+    int out_type;
+};
+hipError_t launch_cache_read_q8(const Read8Args& a, hipStream_t st);
+
+struct VerifyArgs {
+    const void* logits;
+    int logits_type;
+    int64_t T, V, ldl;
+    const int32_t* q_start;
+    int B, max_q;
+    const int32_t* tokens;
+    const float* draft;
+    int64_t ldd;
+    const float* u;
+    const float* temperature;
+    int32_t* accepted;
+    int32_t* next;
+    void* ws;
+    int64_t ws_bytes;
+};
+hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st);
+
 }  // namespace qgemv

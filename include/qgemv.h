@@ -516,6 +516,109 @@ qgemv_status qgemm_quantize_w8a8(const int8_t* w, int64_t ldw, const float* sw, 
                                  int y_type, int64_t ldy, void* ws, int64_t ws_bytes,
                                  qgemv_stream_t stream);
 
+/* A paged cache in 8 bits: as qgemv_kv_cache, with every row of head_dim values
+ * (one head of one slot, of k or of v) as int8 codes and one fp32 scale; the
+ * row's values are code * scale.  Code e of head h in slot t of page p is at byte
+ * p * page_stride + t * token_stride + h * head_stride + e of k (or v), the row's
+ * scale at element p * scale_page_stride + t * scale_token_stride + h *
+ * scale_head_stride of k_scale (or v_scale).  k, v: 16-byte aligned; strides of
+ * codes: multiples of 16; head_dim: a multiple of 16, at most QGEMV_HEAD_DIM_MAX;
+ * scales: 4-byte aligned.  Other limits as for qgemv_kv_cache.  A row takes
+ * head_dim + 4 bytes, where 16 bits take 2 * head_dim. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    int32_t n_pages, page_size, heads, head_dim;
+} qgemv_kv_cache_q8;
+
+/* qgemv_rope_append into an 8-bit cache: rows of k, rotated, and of v are
+ * quantised as they are written, each by itself, as qgemv_quantize_rows does it:
+ * scale = max|y| / 127, code = clamp(round_half_away(y / scale), -127, 127), both
+ * quotients IEEE fp32 divisions; a row of zeros has scale 0 and codes 0.  (Values
+ * are meant to be finite: an infinity makes its row's scale infinite, and a NaN's
+ * code means nothing; other rows are not touched by them.)  The angle pos[t] *
+ * inv_freq[i] is formed in 64 bits, its sine and cosine are rounded to fp32, and
+ * x_i c - x_j s and x_j c + x_i s are formed in 64 bits and rounded once to fp32, so
+ * that a code next to a border does not hang on an order of roundings.
+ *   q_type: QGEMV_TYPE_F16 or _BF16; q_out: [T][ldqo] of q_type.
+ * All other arguments, limits and errors as for qgemv_rope_append. */
+qgemv_status qgemv_rope_append_q8(const qgemv_kv_cache_q8* cache, int64_t T, int in_type,
+                                  const void* q, int64_t ldq, int q_heads, const void* k,
+                                  int64_t ldk, const void* v, int64_t ldv, const int32_t* pos,
+                                  const int64_t* slots, const float* inv_freq, int rot_dim,
+                                  int style, void* q_out, int q_type, int64_t ldqo,
+                                  qgemv_stream_t stream);
+
+/* qgemv_paged_attn over an 8-bit cache: the same sequences, places, windows, sinks
+ * and tables, with k_j and v_j the values of the cache's rows and q of q_type
+ * (QGEMV_TYPE_F16 or _BF16).  Codes enter the matrix cores as they are (whole
+ * numbers, exact in fp16) and q without a rounding that counts (a bf16 row as fp16
+ * times a power of two: values below 2^-38 of the row's largest may be lost), a key's scale is
+ * multiplied to its score in fp32, and a value's scale to its weight, which is then
+ * rounded to fp16 (scaled by powers of two, so that what is lost is below 2^-27
+ * of the row's largest weight times its largest seen scale).  Scales of values are
+ * meant to be below 2^60, and what scales below 2^-60 contribute may be lost.
+ * Argument conventions, limits and errors as for qgemv_paged_attn. */
+qgemv_status qgemv_paged_attn_q8(const qgemv_kv_cache_q8* cache, const void* q, int q_type,
+                                 int64_t T, int64_t ldq, int q_heads, const int32_t* q_start,
+                                 const int32_t* kv_len, int B, int max_q, int64_t max_kv,
+                                 const int32_t* table, int64_t ldt, float scale, int window,
+                                 int sinks, void* out, int out_type, int64_t ldo, float* lse,
+                                 void* ws, int64_t ws_bytes, qgemv_stream_t stream);
+
+/* Rows of an 8-bit cache as plain rows again: for t < T, k_out[t] and v_out[t]
+ * (all heads of slot slots[t], head after head) = code * scale in fp32, rounded
+ * once to out_type.  A slot that is negative or past the pool gives rows of zeros;
+ * slots may repeat.  slots: int64 [T]; k_out, v_out: [T][ldk], [T][ldv] of out_type,
+ * 16-byte aligned with rows of a multiple of 16 bytes; either may be NULL (its row
+ * stride is then not looked at).  T at most 2^28. */
+qgemv_status qgemv_cache_read_q8(const qgemv_kv_cache_q8* cache, int64_t T, const int64_t* slots,
+                                 void* k_out, int64_t ldk, void* v_out, int64_t ldv, int out_type,
+                                 qgemv_stream_t stream);
+
+/* Verification of drafted tokens (speculative decoding).  Sequence b brings the
+ * rows q_start[b] .. q_start[b + 1] - 1 (n of them): its last token and then n - 1
+ * drafted ones, tokens[r] being the token of row r and logits[r] what the model
+ * says after it.  With temperature t = temperature[b],
+ *     p_r(v) = exp(logits[r][v] / t) / sum_w exp(logits[r][w] / t)
+ * and draft[r] the probabilities that token r was drawn from, draft i (row r =
+ * q_start[b] + i, i = 1 .. n - 1) is accepted while all before it were, if
+ *     u[r] * draft[r][tokens[r]] < p_{r-1}(tokens[r]).
+ * accepted[b] is how many are.  next[b] is the token after them, from the row r =
+ * q_start[b] + accepted[b]: of the weights w_v = p_r(v) if all drafts were accepted,
+ * and w_v = max(p_r(v) - draft[r + 1][v], 0) otherwise (p_r(v) where that leaves
+ * nothing), the first v with
+ *     w_0 + .. + w_v > u[q_start[b]] * (w_0 + .. + w_{V-1}),
+ * the last one whose weight is not 0 where there is none (u of 1 or above).  The
+ * accepted tokens and the next one are then distributed as tokens drawn from p.
+ * Exponentials and sums are 64-bit.
+ *   A temperature that is not above 0 means p_r = 1 at the first of the largest logits
+ *   and 0 elsewhere.  A logit of -inf or NaN has p = 0 (of +inf: all of the mass, shared
+ *   among its like); a row without any other has no mass: nothing is accepted
+ *   from it and next[b] = -1.  A draft probability that is not above 0 (or NaN) is 0.
+ *   A sequence without rows gets accepted = 0 and next = -1.
+ *   logits: [T][ldl] of logits_type, V values a row, aligned to their elements.
+ *   q_start: int32 [B + 1], held to [0, T]; max_q: at least the most rows of a
+ *      sequence (rows past it are not looked at).
+ *   tokens: int32 [T] (those of first rows are not looked at); one outside [0, V) is
+ *      not accepted.  u: fp32 [T] in [0, 1), independent: that of a draft's row is for
+ *      its acceptance, that of a first row for next.
+ *   draft: fp32 [T][ldd] (first rows are not looked at), or NULL where the drafted
+ *      tokens were certain: probability 1 for tokens[r], 0 for others.
+ *   temperature: fp32 [B], or NULL for 1.  accepted, next: int32 [B].
+ *   ws: as for qgemv_paged_attn; without enough a sequence is one workgroup's work.
+ * Limits: T at most 2^28, V at most 2^24, B and max_q at most 65535. */
+qgemv_status qgemv_verify_draft(const void* logits, int logits_type, int64_t T, int64_t V,
+                                int64_t ldl, const int32_t* q_start, int B, int max_q,
+                                const int32_t* tokens, const float* draft, int64_t ldd,
+                                const float* u, const float* temperature, int32_t* accepted,
+                                int32_t* next, void* ws, int64_t ws_bytes,
+                                qgemv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
