@@ -3,7 +3,16 @@
 // visible.
 //
 // With codes ck, cv and scales sk, sv: x_j = scale sk_j (q . ck_j), m their
-// largest, w_j = exp(x_j - m), out = sum w_j sv_j cv_j / sum w_j.
+// largest, w_j = exp(x_j - m), out = sum w_j sv_j cv_j / sum w_j, in one pass over
+// the keys with the running maximum and sum of a softmax.  Codes are whole numbers
+// that fp16 holds, so they go to the fp16 matrix cores exactly and the scales are
+// taken in fp32 on both sides of them: a key's multiplies its score, a value's its
+// weight.  The weight is then rounded to fp16, with factors of two that keep it in
+// fp16's range (kLift, and the largest scale that the row has seen).
+//
+// Rows, tiles and their order are those of the attention over 16-bit values: the
+// queries of a sequence times the G query heads of a cache head, 32 rows a wave, X^T
+// = K Q^T (keys down, rows across), O^T += V^T P^T.
 #include "qgemv_attn.h"
 
 namespace qgemv {
@@ -81,18 +90,685 @@ __device__ void attn8_row(const Attn8Dev& a, const Span& s, const int32_t* table
     }
 }
 
-// A wave a row.
-template <typename T, typename TO>
-__global__ __launch_bounds__(64) void k_attn8_rows(const Attn8Dev a) {
-    const int b = blockIdx.y;
-    for (int r = blockIdx.x; r < a.max_q * a.q_heads; r += gridDim.x) {
-        const int i = r / a.q_heads, hq = r - i * a.q_heads;
-        Span s;
-        if (!make_span<64, 1>(a, b, i * a.G, 0, s)) return;
-        float o[4], m, l;
-        attn8_row<T, 64>(a, s, a.table + b * a.ldt, i, hq, a.scale * 1.4426950408889634f, o, m, l);
-        put_row<TO>(a, s, 0, i, hq, o, m, l);
+// A code and a half are one number: 1024 + (code + 128) in fp16 is 0x6400 with the
+// code's byte, its top bit turned over, in the low bits; 1152 less is the code.
+// Five instructions for four codes.
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi) {
+    const f16x2 off = {(f16)-1152.f, (f16)-1152.f};
+    const uint32_t w[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
+    union { f16x2 h[4]; f16x8 v; } r;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        r.h[2 * i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u)) + off;
+        r.h[2 * i + 1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u)) + off;
     }
+    return r.v;
+}
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// What weights may grow to before o and l are scaled, and the weight of the maximum:
+// 2^7 to 2^15, so that fp16 (2^-24 to 2^16) holds what is above 2^-32 of a row's
+// largest.  A weight times a value's scale is held there by 2^-r, 2^r the first power
+// of two that no seen scale of the row exceeds; l takes the same factor, which so
+// falls out of o / l.  r is kept as a float's exponent field, in -60 .. 60 (larger
+// scales overflow and are left to attn8_row; what smaller ones add may be lost).
+constexpr float kSlack8 = 8.f, kLift8 = 7.f;
+constexpr int kLeast = 127 - 60, kMost = 127 + 60;
+
+// Where chunks of 16 bytes of a row stand: chunk c of row r of an LDS tile at place c
+// ^ f(r) of the row.  Codes (rows of DP bytes): 16 lanes that read one chunk of
+// 16 keys, and the 16 keys times 32 bytes of a transposing read by half waves, fall on
+// all places of 256 bytes.
+template <int DP> struct Place8 {
+    static __device__ __forceinline__ int k(int r) { return DP == 64 ? (r >> 2) & 3 : DP == 128 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ int v(int r) {
+        return DP == 64 ? (r >> 3 & 1) << 1 : DP == 128 ? (r >> 1 & 1) << 1 | (r >> 3 & 1) << 2 : (r & 3) << 1 | (r >> 3 & 1) << 3;
+    }
+};
+// Halves (rows of 2 DP bytes): the same for reads, and for writes of a row's
+// chunks by every second.
+template <int DP> struct Place16 {
+    static __device__ __forceinline__ int k(int r) { return DP == 64 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ int v(int r) { return DP == 64 ? (r >> 1 & 1) * 5 : (r & 3) << 2 | ((r >> 2 ^ r) & 3); }
+};
+
+// What a wave holds of its 32 rows, and the steps of a tile of KT keys.
+template <int DP, int KT>
+struct Rows8 {
+    static constexpr int ND = DP / 32, NX = KT / 32, NS = DP / 16;
+    f16x8 qf[NS];
+    f32x16 o[ND];
+    float m, l;
+    int r;                       // exponent field of the scales' factor
+    float c2;                    // what scores are multiplied by: |scale| log2(e), and q's factor
+    int p, z, p_lo, p_hi, z_hi;  // place and window start of this lane's row, and of the wave's rows
+                                 // (p_lo: below every key for a scale of 0, so that weights looks at every tile)
+
+    // The rows first_row .. first_row + 31 of the block; this lane's is `row`.  A
+    // lane has, of each 32 dimensions, the 16 from `first` on: in two runs of 8
+    // that lie together (JOINED, as a read of 16 codes leaves them) or 16 apart.
+    template <typename T, bool JOINED>
+    __device__ __forceinline__ void start(const AttnDev& a, const Span& s, int h, int row, int first_row) {
+        const int lane = threadIdx.x & 63, half = lane >> 5;
+        const int qi = row / a.G, hq = h * a.G + row - qi * a.G;
+        p = s.place(qi);
+        z = window_start(a, p);
+        p_lo = a.scale == 0.f ? INT32_MIN : s.place(min(first_row / a.G, s.i1));
+        p_hi = s.place(min((first_row + 31) / a.G, s.i1));
+        z_hi = window_start(a, p_hi);
+        // (the sign of the scale is moved into q; a scale of 0 is taken in weights, because
+        // the -inf of a hidden key times 0 would be NaN)
+        c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
+        const T* q = (const T*)a.q + (int64_t)(s.s0 + qi) * a.ldq + (int64_t)hq * a.D;
+        typedef T V8 __attribute__((ext_vector_type(8)));
+        V8 in[NS];
+#pragma unroll
+        for (int k = 0; k < NS; k++) {
+            const int d = JOINED ? 32 * (k / 2) + 16 * half + 8 * (k % 2) : 16 * k + 8 * half;
+            in[k] = V8{};
+            if (d < a.D) in[k] = *reinterpret_cast<const V8*>(q + d);
+        }
+        float f = a.scale < 0.f ? -1.f : 1.f;
+        if constexpr (std::is_same<T, bf16>::value) {
+            // bf16 as fp16 times a power of two that takes the row's largest value to 2^14
+            // .. 2^15: eight bits of each value then stand down to 2^-31 of it, and what is
+            // below 2^-39 of it is lost
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < NS; k++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf((float)in[k][e]));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // (rows of zeros, rows below 2^-99 and what is not finite: a factor within the range)
+            int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23);
+            e = e == 255 ? 127 + 14 : max(e, 27);
+            f *= __builtin_bit_cast(float, (uint32_t)(127 + 14 + 127 - e) << 23);
+            c2 *= __builtin_bit_cast(float, (uint32_t)(e - 14) << 23);
+        }
+#pragma unroll
+        for (int k = 0; k < NS; k++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) qf[k][e] = (f16)((float)in[k][e] * f);
+#pragma unroll
+        for (int d = 0; d < ND; d++) o[d] = f32x16{};
+        m = -INFINITY;
+        l = 0.f;
+        r = kLeast;
+    }
+    // X^T = K Q^T of the codes at lds + AT (JOINED), 32 dimensions a read.
+    template <int AT>
+    __device__ __forceinline__ void scores8(const char* lds, f32x16 (&x)[NX]) {
+        const int half = (threadIdx.x & 63) >> 5, row = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 0; n < NX; n++) {
+            x[n] = f32x16{};
+#pragma unroll
+            for (int k = 0; k < NS / 2; k++) {
+                const char* at = lds + row * DP + ((2 * k + half) ^ Place8<DP>::k(row)) * 16;
+                const u32x4 c = *reinterpret_cast<const u32x4*>(at + AT + 32 * n * DP);
+                x[n] = mfma(halves(c[0], c[1]), qf[2 * k], x[n]);
+                x[n] = mfma(halves(c[2], c[3]), qf[2 * k + 1], x[n]);
+            }
+        }
+    }
+    // The same of halves (not JOINED).
+    template <int AT>
+    __device__ __forceinline__ void scores16(const char* lds, f32x16 (&x)[NX]) {
+        const int half = (threadIdx.x & 63) >> 5, row = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 0; n < NX; n++) {
+            x[n] = f32x16{};
+#pragma unroll
+            for (int k = 0; k < NS; k++) {
+                const char* at = lds + row * DP * 2 + ((2 * k + half) ^ Place16<DP>::k(row)) * 16;
+                x[n] = mfma(*reinterpret_cast<const f16x8*>(at + AT + 32 * n * DP * 2), qf[k], x[n]);
+            }
+        }
+    }
+    // Weights from scores, with the running maximum, sum and scale.  `there` names the
+    // keys of the tile (from j0 on) that have a page, sc their scales: KT of keys, then
+    // of values.
+    __device__ __forceinline__ void weights(const AttnDev& a, const float* sc, int j0, unsigned long long there,
+                                            f32x16 (&x)[NX], f16x8 (&pf)[2 * NX]) {
+        const int half = (threadIdx.x & 63) >> 5;
+        f32x4v sv[NX][4];
+#pragma unroll
+        for (int n = 0; n < NX; n++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const f32x4v sk = *reinterpret_cast<const f32x4v*>(sc + 32 * n + 8 * g + 4 * half);
+                sv[n][g] = *reinterpret_cast<const f32x4v*>(sc + KT + 32 * n + 8 * g + 4 * half);
+#pragma unroll
+                for (int i = 0; i < 4; i++) x[n][4 * g + i] *= sk[i];
+            }
+        const unsigned long long all = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
+        if (!((there & all) == all && j0 + KT - 1 <= p_lo && (j0 >= z_hi || j0 + KT - 1 < a.sinks))) {
+            if (a.scale == 0.f) {
+#pragma unroll
+                for (int n = 0; n < NX; n++) x[n] *= 0.f;
+            }
+            // what the row does not see: a score of -inf, a scale of 0 (whatever they hold)
+            const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+            const unsigned long long seen =
+                (there & below(p - j0 + 1) & (~below(z - j0) | below(a.sinks - j0))) >> (4 * half);
+            const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+#pragma unroll
+            for (int n = 0; n < NX; n++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const bool on = word[n] & (1u << (8 * (e / 4) + e % 4));
+                    x[n][e] = on ? x[n][e] : -INFINITY;
+                    sv[n][e / 4][e % 4] = on ? sv[n][e / 4][e % 4] : 0.f;
+                }
+        }
+        float mt = x[0][0], st = sv[0][0][0];
+#pragma unroll
+        for (int n = 0; n < NX; n++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                mt = fmaxf(mt, x[n][e]);
+                st = fmaxf(st, sv[n][e / 4][e % 4]);
+            }
+        mt = max_halves(mt) * c2;
+        st = max_halves(st);
+        if (__any(mt > m + kSlack8 || st > __builtin_bit_cast(float, r << 23))) {
+            const float mn = fmaxf(m, mt);
+            const int e = (int)((__builtin_bit_cast(uint32_t, fmaxf(st, 0.f)) + 0x7fffffu) >> 23);   // (up to a power of two)
+            const int rn = min(max(r, e), kMost);
+            const float fix = (mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn)) *
+                              __builtin_bit_cast(float, (127 + r - rn) << 23);
+            l *= fix;
+#pragma unroll
+            for (int d = 0; d < ND; d++) o[d] *= fix;
+            m = mn;
+            r = rn;
+        }
+        const float mu = m == -INFINITY ? 0.f : m - kLift8 + (float)(r - 127);
+        // (l takes a tile's weights at once: one by one those below half of its last
+        // bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is)
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NX; n++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(x[n][e], c2, -mu));
+                sum += w;
+                pf[2 * n + e / 8][e % 8] = (f16)(w * sv[n][e / 4][e % 4]);
+            }
+        l += sum;
+    }
+    // After the last tile: l with both halves' keys, and m as what a weight of 1 stands
+    // for, by which parts are joined and lse is formed.
+    __device__ __forceinline__ void finish() {
+        l += __shfl_xor(l, 32);
+        m += (float)(r - 127) - kLift8;
+    }
+    // This lane's part of a transposing read of codes: dimensions 32 d .. 32 d + 31,
+    // sixteen keys.  Of 16 lanes, lane i names 8 bytes of key i / 2 (of eight) and gets
+    // dimension i of all eight.  A half takes the keys whose weights it has: 4 half + 0 ..
+    // 3 and 8 more.
+    __device__ __forceinline__ static uint32_t v_part8(const char* lds, int d) {
+        const int lane = threadIdx.x & 63, half = lane >> 5, g = (lane >> 4) & 1, i = lane & 15;
+        const int key = 4 * half + (i >> 1 & 3) + 8 * (i >> 3);
+        return (uint32_t)(uintptr_t)(lmem*)(lds + key * DP + ((2 * d + g) ^ Place8<DP>::v(key)) * 16 + (i & 1) * 8);
+    }
+    // O^T += V^T P^T of the codes at lds + AT, 16 keys a step.  Other tiles are on their
+    // way to LDS meanwhile, and the compiler would wait for all of them before the reads'
+    // builtin; so two steps of 64 dimensions are read, and waited for, at once.
+    template <int AT>
+    __device__ __forceinline__ void add8(const char* lds, const f16x8 (&pf)[2 * NX]) {
+        static_assert(AT + KT * DP <= 65536, "offsets of a read");
+        two_steps8<AT, 0>(lds, pf);
+        if constexpr (NX == 2) two_steps8<AT, 2>(lds, pf);
+    }
+    template <int AT, int U>
+    __device__ __forceinline__ void two_steps8(const char* lds, const f16x8 (&pf)[2 * NX]) {
+#pragma unroll
+        for (int d = 0; d < ND; d += 2) {
+            u32x2 v[2][2];   // [step][dimensions]
+            asm volatile(
+                "ds_read_b64_tr_b8 %0, %4 offset:%6\n\tds_read_b64_tr_b8 %1, %5 offset:%6\n\t"
+                "ds_read_b64_tr_b8 %2, %4 offset:%7\n\tds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
+                : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
+                : "memory");
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) o[d + c] = mfma(halves(v[u][c][0], v[u][c][1]), pf[U + u], o[d + c]);
+        }
+    }
+    // The same of halves: keys 8 w + 4 half .. + 3 of sixteen a read.
+    __device__ __forceinline__ static uint32_t v_part16(const char* lds, int d, int w) {
+        const int lane = threadIdx.x & 63, half = lane >> 5, g = lane >> 4, i = lane & 15;
+        const int key = 8 * w + 4 * half + (i >> 2);
+        const int chunk = 4 * d + 2 * (g & 1) + ((i & 3) >> 1);
+        return (uint32_t)(uintptr_t)(lmem*)(lds + key * DP * 2 + (chunk ^ Place16<DP>::v(key)) * 16 + (i & 1) * 8);
+    }
+    template <int AT>
+    __device__ __forceinline__ void add16(const char* lds, const f16x8 (&pf)[2 * NX]) {
+        static_assert(AT + KT * DP * 2 <= 65536, "offsets of a read");
+        two_steps16<AT, 0>(lds, pf);
+        if constexpr (NX == 2) two_steps16<AT, 2>(lds, pf);
+    }
+    template <int AT, int U>
+    __device__ __forceinline__ void two_steps16(const char* lds, const f16x8 (&pf)[2 * NX]) {
+#pragma unroll
+        for (int d = 0; d < ND; d += 2) {
+            s16x4 v[2][2][2];   // [step][dimensions][eight keys]
+            asm volatile(
+                "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
+                "ds_read_b64_tr_b16 %2, %10 offset:%12\n\tds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
+                "ds_read_b64_tr_b16 %4, %8 offset:%13\n\tds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
+                "ds_read_b64_tr_b16 %6, %10 offset:%13\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(v[0][0][0]), "=&v"(v[0][0][1]), "=&v"(v[0][1][0]), "=&v"(v[0][1][1]),
+                  "=&v"(v[1][0][0]), "=&v"(v[1][0][1]), "=&v"(v[1][1][0]), "=&v"(v[1][1][1])
+                : "v"(v_part16(lds, d, 0)), "v"(v_part16(lds, d, 1)), "v"(v_part16(lds, d + 1, 0)),
+                  "v"(v_part16(lds, d + 1, 1)), "n"(AT + U * 16 * DP * 2), "n"(AT + (U + 1) * 16 * DP * 2)
+                : "memory");
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) o[d + c] = mfma(__builtin_bit_cast(f16x8, v[u][c]), pf[U + u], o[d + c]);
+        }
+    }
+};
+
+// Where keys that are not there and dimensions past the head's come from.
+__device__ const uint4 g_zeros8[QGEMV_HEAD_DIM_MAX / 16] = {};
+
+// The pages of a tile's keys, from 64 columns of the table at a time (one a
+// lane): a tile's columns are within 64 even with a page for every key.  A tile
+// whose keys are all there, in pages of whole runs of 16 (a.runs), is addressed
+// by scalars: one page and one base a run.  Any other has an offset for every
+// key.
+template <int DP, int KT>
+struct Pages8 {
+    int first = -64, page = -1;            // the lane's column is first + lane
+    unsigned long long valid = 0;          // columns with a page of the pool
+    int j0;                                // the tile: its first key
+    bool runs;                             // whether scalars do
+    int64_t off, soff;                     // offsets of the codes and the scale of key `lane`, -1 where it is not there
+
+    __device__ __forceinline__ void ask(const AttnDev& a, const int32_t* table) {
+        const int lane = threadIdx.x & 63;
+        first = 0;
+        if (lane < a.ldt) page = table[lane];
+    }
+    __device__ __forceinline__ void arrive(const AttnDev& a) { valid = __ballot(page >= 0 && page < a.n_pages); }
+
+    // Takes up the tile at key j; returns which of its keys are there.
+    __device__ __forceinline__ unsigned long long tile(const Attn8Dev& a, const Span& s, const int32_t* table, int j) {
+        const int lane = threadIdx.x & 63;
+        j0 = j;
+        off = soff = -1;
+        const int c0 = a.page_shift >= 0 ? j0 >> a.page_shift : j0 / a.page_size;
+        const int c1 = a.page_shift >= 0 ? (j0 + KT - 1) >> a.page_shift : (j0 + KT - 1) / a.page_size;
+        if (c0 < first || c1 >= first + 64) {
+            first = c0;
+            page = first + lane < a.ldt ? table[first + lane] : -1;
+            arrive(a);   // (the wait for the page is here, not at every tile)
+        }
+        const unsigned long long need = (2ull << (c1 - c0)) - 1;
+        runs = a.runs && j0 + KT <= s.limit && (valid >> (c0 - first) & need) == need;
+        if (runs) return ~0ull;
+        const int key = j0 + (KT == 64 ? lane : lane & (KT - 1));
+        const int c = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
+        const int mine = __shfl(page, c - first);
+        if (key < s.limit && mine >= 0 && mine < a.n_pages) {
+            off = key_offset(a, mine, key);
+            soff = scale_offset(a, mine, key);
+        }
+        return __ballot(off >= 0);
+    }
+    __device__ __forceinline__ int run_page(const AttnDev& a, int key) const {
+        return __builtin_amdgcn_readlane(page, (key >> a.page_shift) - first);
+    }
+
+    // Where this lane's 16 codes of COUNT loads of the tile's K or V are, from row row0
+    // on, 1 KB of rows a load: f(load, address).  `swizzle` says which chunk of its row a
+    // lane takes.
+    template <int COUNT, typename S, typename F>
+    __device__ __forceinline__ void walk(const AttnDev& a, const char* from, int row0, S swizzle, F f) const {
+        constexpr int CPR = DP / 16, RPI = 64 / CPR;
+        if (__builtin_expect(runs, 1)) {
+            const int lane = threadIdx.x & 63, lr = lane / CPR, lc = lane % CPR;
+            constexpr int RUN = COUNT * RPI < 16 ? COUNT : 16 / RPI;   // loads of (part of) a run
+            static_assert(COUNT % RUN == 0, "whole runs");
+            const uint32_t stride = (uint32_t)a.token_stride;
+#pragma unroll
+            for (int r = 0; r < COUNT / RUN; r++) {
+                const int key = j0 + row0 + RUN * RPI * r;
+                const char* base = from + (run_page(a, key) * a.page_stride + (key & (a.page_size - 1)) * a.token_stride);
+#pragma unroll
+                for (int c = 0; c < RUN; c++) {
+                    const int row = row0 + RUN * RPI * r + RPI * c;
+                    uint32_t at = (RPI * c + lr) * stride + 16 * (lc ^ swizzle(row | lr));
+                    asm volatile("" : "+v"(at));   // (32 bits to keep, not an address)
+                    f(RUN * r + c, base + at);
+                }
+            }
+            return;
+        }
+        // (hidden from the compiler, which would form addresses for this branch
+        // ahead of the loop over tiles, in registers that the others need)
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int lr = lane / CPR, lc = lane % CPR;
+#pragma unroll
+        for (int c = 0; c < COUNT; c++) {
+            const int row = row0 + RPI * c + lr;
+            const int64_t at = __shfl((long long)off, row);
+            const int chunk = lc ^ swizzle(row);
+            const char* g = from + (at + 16 * chunk);
+            f(c, at >= 0 && 16 * chunk < a.D ? g : (const char*)g_zeros8);
+        }
+    }
+    // Where the scale of key `row` of the tile is (of the array `from`, at its head's).
+    __device__ __forceinline__ const float* scale(const Attn8Dev& a, const float* from, int row) const {
+        if (__builtin_expect(runs, 1)) {
+            const float* base[KT / 16];
+#pragma unroll
+            for (int u = 0; u < KT / 16; u++) {
+                const int key = j0 + 16 * u;
+                base[u] = from + (run_page(a, key) * a.scale_page_stride + (key & (a.page_size - 1)) * a.scale_token_stride);
+            }
+            const float* b = base[0];
+#pragma unroll
+            for (int u = 1; u < KT / 16; u++) b = row / 16 == u ? base[u] : b;
+            return b + (uint32_t)(row & 15) * (uint32_t)a.scale_token_stride;
+        }
+        const int64_t at = __shfl((long long)soff, row);
+        return at >= 0 ? from + at : (const float*)g_zeros8;
+    }
+};
+
+__device__ __forceinline__ void to_lds16(const void* from, char* to) {
+    __builtin_amdgcn_global_load_lds((gmem*)from, (lmem*)to, 16, 0, 0);
+}
+
+// Many rows: NW waves of 32 rows each, which share every tile of KT keys.  The codes
+// of the next tile are on their way to registers while one is used, and are made fp16
+// once for all waves, on their way to LDS.
+template <typename T, typename TO, int DP, int KT, int NW, int OCC>
+__global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
+    typedef Rows8<DP, KT> R;
+    constexpr int ROWS = 32 * NW, CPR = DP / 16, RPI = 64 / CPR;
+    constexpr int TILE = KT * DP * 2, BUF = 2 * TILE;    // bytes of a K (or V) tile, and of both
+    constexpr int LOADS = KT / RPI / NW;                 // wave loads of K (and of V) per wave
+    constexpr int SC = 2 * KT;                           // scales of a tile
+    static_assert(LOADS >= 1 && KT <= 64 && SC <= 64 * NW, "tile shape");
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    float* sc = reinterpret_cast<float*>(lds + 2 * BUF);
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+    // heads first, so that the workgroups of one head meet in one L2; the row
+    // tiles with the most keys first
+    const int h = blockIdx.x % a.heads;
+    const int rest = blockIdx.x / a.heads;
+    const int part = rest % a.splits, row_tile = a.row_tiles - 1 - rest / a.splits;
+    const int b = blockIdx.y;
+    const int32_t* table = a.table + b * a.ldt;
+    Pages8<DP, KT> pages;
+    pages.ask(a, table);
+    Span s;
+    if (!make_span<KT, ROWS>(a, b, row_tile, part, s)) return;
+
+    // this lane's row, the last one of the block where it has none of its own
+    const int first_row = row_tile * ROWS + 32 * wave, r = first_row + (lane & 31);
+    const int r_end = (s.i1 + 1) * a.G;
+    const int rc = min(r, r_end - 1);
+    const bool active = first_row < r_end;
+    R w;
+    w.template start<T, false>(a, s, h, rc, first_row);
+    pages.arrive(a);
+
+    const char* kbase = (const char*)a.k + h * a.head_stride;
+    const char* vbase = (const char*)a.v + h * a.head_stride;
+    const float* sbase = (threadIdx.x < KT ? a.ks : a.vs) + h * a.scale_head_stride;
+    u32x4 kc[LOADS], vc[LOADS];
+    float scale;
+    const auto plain = [](int) { return 0; };
+    auto ask_tile = [&](int t) -> unsigned long long {
+        const unsigned long long there = pages.tile(a, s, table, tile_of(s, t) * KT);
+        pages.template walk<LOADS>(a, kbase, RPI * LOADS * wave, plain,
+                                   [&](int c, const char* g) { kc[c] = *reinterpret_cast<const u32x4*>(g); });
+        pages.template walk<LOADS>(a, vbase, RPI * LOADS * wave, plain,
+                                   [&](int c, const char* g) { vc[c] = *reinterpret_cast<const u32x4*>(g); });
+        const float* g = pages.scale(a, sbase, threadIdx.x & (KT - 1));
+        if (threadIdx.x < SC) scale = *g;
+        return there;
+    };
+    // (a row's chunk c of 16 codes becomes its chunks 2 c and 2 c + 1 of eight halves)
+    auto put_tile = [&](int buf) {
+        char* to = lds + buf * BUF;
+#pragma unroll
+        for (int c = 0; c < LOADS; c++) {
+            const int row = RPI * (LOADS * wave + c) + lane / CPR, chunk = 2 * (lane % CPR);
+            char* k = to + row * DP * 2;
+            char* v = k + TILE;
+            *reinterpret_cast<f16x8*>(k + (chunk ^ Place16<DP>::k(row)) * 16) = halves(kc[c][0], kc[c][1]);
+            *reinterpret_cast<f16x8*>(k + (chunk + 1 ^ Place16<DP>::k(row)) * 16) = halves(kc[c][2], kc[c][3]);
+            *reinterpret_cast<f16x8*>(v + (chunk ^ Place16<DP>::v(row)) * 16) = halves(vc[c][0], vc[c][1]);
+            *reinterpret_cast<f16x8*>(v + (chunk + 1 ^ Place16<DP>::v(row)) * 16) = halves(vc[c][2], vc[c][3]);
+        }
+        if (threadIdx.x < SC) sc[buf * SC + threadIdx.x] = scale;
+    };
+
+    unsigned long long there = 0, there_next = 0;
+    if (s.t0 < s.t1) {
+        there = ask_tile(s.t0);
+        put_tile(0);
+    }
+    __syncthreads();
+    auto step = [&](int t, auto buf) {
+        constexpr int AT = buf * BUF;
+        if (t + 1 < s.t1) there_next = ask_tile(t + 1);
+        const int j0 = tile_of(s, t) * KT;
+        if (active && j0 <= w.p_hi && (j0 + KT > window_start(a, w.p_lo) || j0 < a.sinks)) {
+            f32x16 x[R::NX];
+            f16x8 pf[2 * R::NX];
+            w.template scores16<AT>(lds, x);
+            w.weights(a, sc + buf * SC, j0, there, x, pf);
+            w.template add16<AT + TILE>(lds, pf);
+        }
+        if (t + 1 < s.t1) put_tile(1 - buf);
+        __syncthreads();
+        there = there_next;
+    };
+    for (int t = s.t0; t < s.t1; t += 2) {
+        step(t, std::integral_constant<int, 0>{});
+        if (t + 1 < s.t1) step(t + 1, std::integral_constant<int, 1>{});
+    }
+    if (!active) return;
+    w.finish();
+
+    bool bad = false;
+#pragma unroll
+    for (int d = 0; d < R::ND; d++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) bad |= !(fabsf(w.o[d][e]) < INFINITY);
+    bad |= !(fabsf(w.l) < INFINITY);
+    bad |= __shfl_xor((int)bad, 32);
+    const bool own = r < r_end;
+    const int qi = rc / a.G, hq = h * a.G + rc - qi * a.G;
+    const int64_t tok = s.s0 + qi, row = tok * a.q_heads + hq;
+    if (own && !bad) {
+        const int64_t at = row * a.splits + part;
+        const float inv = s.parts > 1 ? 1.f : row_scale(w.l);
+        TO* out = (TO*)a.out + tok * a.ldo + (int64_t)hq * a.D;
+#pragma unroll
+        for (int d = 0; d < R::ND; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int d0 = 32 * d + 8 * e + 4 * half;
+                if (d0 >= a.D) continue;
+                const float f[4] = {w.o[d][4 * e] * inv, w.o[d][4 * e + 1] * inv,
+                                    w.o[d][4 * e + 2] * inv, w.o[d][4 * e + 3] * inv};
+                if (s.parts > 1) store4(a.part_o + at * a.D + d0, f);
+                else store4(out + d0, f);
+            }
+        if (half == 0) {
+            if (s.parts > 1) {
+                a.part_ml[2 * at] = w.m;
+                a.part_ml[2 * at + 1] = w.l;
+            } else if (a.lse) {
+                a.lse[row] = row_lse(w.m, w.l);
+            }
+        }
+    }
+    for (unsigned todo = (unsigned)__ballot(own && bad); todo; todo &= todo - 1) {
+        const int rr = first_row + __builtin_ctz(todo);
+        const int i = rr / a.G, hh = h * a.G + rr - i * a.G;
+        float ro[4], rm, rl;
+        attn8_row<T, KT>(a, s, table, i, hh, a.scale * 1.4426950408889634f, ro, rm, rl);
+        put_row<TO>(a, s, part, i, hh, ro, rm, rl);
+    }
+}
+
+// At most 32 rows: each of NW waves takes a run of the tiles.  Its ring holds codes
+// and scales of two tiles, straight from memory; a tile's K and scales make room for
+// those after next as soon as the scores are formed, and V likewise, so that most
+// of it is always on its way.  Codes become fp16 between LDS and the matrix cores.
+template <typename T, typename TO, int DP, int NW>
+__global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8Dev a) {
+    constexpr int KT = 32, ROWS = 32;
+    typedef Rows8<DP, KT> R;
+    constexpr int TILE = KT * DP, SCB = 2 * KT * 4, RING = 4 * TILE + 2 * SCB;   // K, K, V, V, scales, scales
+    constexpr int RPI = 64 / (DP / 16), LOADS = KT / RPI;                       // wave loads of a tile
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, row32 = lane & 31;
+    const int h = blockIdx.x % a.heads, part = blockIdx.x / a.heads, b = blockIdx.y;
+    const int32_t* table = a.table + b * a.ldt;
+    Pages8<DP, KT> pages;
+    Span s;
+    if (!make_span<KT, ROWS>(a, b, 0, part, s)) return;
+    const int rows = (s.i1 + 1) * a.G;
+    R w;
+    w.template start<T, true>(a, s, h, min(row32, rows - 1), 0);
+
+    const char* kbase = (const char*)a.k + h * a.head_stride;
+    const char* vbase = (const char*)a.v + h * a.head_stride;
+    const float* sbase = (half ? a.vs : a.ks) + h * a.scale_head_stride;
+    char* mine = lds + wave * RING;
+    const int each = (s.t1 - s.t0 + NW - 1) / NW;
+    const int t0 = min(s.t0 + wave * each, s.t1), t1 = min(t0 + each, s.t1);
+    auto take = [&](int t) { return pages.tile(a, s, table, tile_of(s, t) * KT); };
+    auto load_k = [&](int slot) {
+        char* to = mine + slot * TILE;
+        pages.template walk<LOADS>(a, kbase, 0, Place8<DP>::k, [&](int c, const char* g) { to_lds16(g, to + 1024 * c); });
+        __builtin_amdgcn_global_load_lds((gmem*)pages.scale(a, sbase, row32), (lmem*)(mine + 4 * TILE + slot * SCB), 4, 0, 0);
+    };
+    auto load_v = [&](int slot) {
+        char* to = mine + (2 + slot) * TILE;
+        pages.template walk<LOADS>(a, vbase, 0, Place8<DP>::v, [&](int c, const char* g) { to_lds16(g, to + 1024 * c); });
+    };
+    if (t0 < t1) {
+        unsigned long long there[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (t0 + i >= t1) break;
+            there[i] = take(t0 + i);
+            load_k(i);
+            load_v(i);
+        }
+        auto step = [&](int t, auto at) {
+            constexpr int SLOT = at;
+            f32x16 x[R::NX];
+            f16x8 pf[2 * R::NX];
+            // (loads land in their order: K S V of this tile, K S V of the next, K S of the one after)
+            const int left = t1 - 1 - t;
+            if (left > 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * LOADS + 1) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+            w.template scores8<SLOT * TILE>(mine, x);
+            w.weights(a, reinterpret_cast<const float*>(mine + 4 * TILE + SLOT * SCB), tile_of(s, t) * KT, there[0], x, pf);
+            QGEMV_WAIT("lgkmcnt(0)");
+            there[0] = there[1];
+            if (left > 1) {
+                there[1] = take(t + 2);
+                load_k(SLOT);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * LOADS + 2) : "memory");
+            } else if (left > 0) {
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS + 1) : "memory");
+            } else {
+                QGEMV_WAIT("vmcnt(0)");
+            }
+            w.template add8<(2 + SLOT) * TILE>(mine, pf);
+            QGEMV_WAIT("lgkmcnt(0)");
+            if (left > 1) load_v(SLOT);
+        };
+        for (int t = t0; t < t1; t += 2) {
+            step(t, std::integral_constant<int, 0>{});
+            if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>{});
+        }
+        w.finish();
+    }
+
+    // the waves' parts of the rows meet in LDS
+    constexpr int LD = DP + 4;
+    static_assert(32 * LD * 4 <= RING, "a wave's result fits its ring");
+    float* po = reinterpret_cast<float*>(mine);
+    float* ml = reinterpret_cast<float*>(lds + NW * RING);   // [NW][2][32]
+#pragma unroll
+    for (int d = 0; d < R::ND; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const f32x4v f = {w.o[d][4 * e], w.o[d][4 * e + 1], w.o[d][4 * e + 2], w.o[d][4 * e + 3]};
+            *reinterpret_cast<f32x4v*>(po + row32 * LD + 32 * d + 8 * e + 4 * half) = f;
+        }
+    if (half == 0) {
+        ml[wave * 64 + row32] = w.m;
+        ml[wave * 64 + 32 + row32] = w.l;
+    }
+    __syncthreads();
+    for (int rr = wave; rr < rows; rr += NW) {
+        float top = -INFINITY, sum = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NW; i++) top = fmaxf(top, ml[i * 64 + rr]);
+#pragma unroll
+        for (int i = 0; i < NW; i++) {
+            const float mi = ml[i * 64 + rr];
+            const float fix = mi == top ? 1.f : exp2f(mi - top);
+            sum += ml[i * 64 + 32 + rr] * fix;
+            const float* src = reinterpret_cast<const float*>(lds + i * RING) + rr * LD;
+#pragma unroll
+            for (int c = 0; c < DP / 64; c++) f[c] += src[lane + 64 * c] * fix;
+        }
+        bool bad = !(fabsf(sum) < INFINITY);
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++) bad |= !(fabsf(f[c]) < INFINITY);
+        const int i = rr / a.G, hh = h * a.G + rr - i * a.G;
+        if (__any(bad))
+            attn8_row<T, KT>(a, s, table, i, hh, a.scale * 1.4426950408889634f, f, top, sum);
+        put_row<TO>(a, s, part, i, hh, f, top, sum);
+    }
+}
+
+template <typename T, typename TO, int DP, int KT, int OCC>
+static void launch_many(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
+    constexpr int NW = 4, ROWS = 32 * NW;
+    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC, DP == 64 ? 1024 : 0, a.ws_bytes, a.ws);
+    launch_kernel(k_attn8_many<T, TO, DP, KT, NW, OCC>,
+                  dim3((unsigned)(d.heads * d.splits * d.row_tiles), (unsigned)d.B), dim3(64 * NW),
+                  2 * (2 * KT * DP * 2 + 2 * KT * 4), st, d);
+    join<TO, KT, ROWS, DP / 4>(d, st);
+}
+template <typename T, typename TO, int DP, int NW>
+static void launch_few(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
+    split(d, a.max_kv, 32, 32, 4 * NW, 256, 0, a.ws_bytes, a.ws);
+    launch_kernel(k_attn8_few<T, TO, DP, NW>, dim3((unsigned)(d.heads * d.splits), (unsigned)d.B),
+                  dim3(64 * NW), NW * (4 * 32 * DP + 512 + 256), st, d);
+    join<TO, 32, 32, DP / 4>(d, st);
 }
 
 hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st) {
@@ -109,11 +785,22 @@ hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st) {
     d.D = a.c.head_dim; d.B = a.B; d.max_q = a.max_q; d.n_pages = a.c.n_pages;
     d.page_size = a.c.page_size; d.window = a.window; d.sinks = a.sinks; d.scale = a.scale;
     d.page_shift = (a.c.page_size & (a.c.page_size - 1)) == 0 ? __builtin_ctz(a.c.page_size) : -1;
-    d.splits = d.split_tiles = 1;
+    d.runs = (d.D == 64 || d.D == 128 || d.D == 256) && d.page_shift >= 4 && d.token_stride < (1 << 26) &&
+             d.scale_token_stride < (1 << 26);
+    const bool few = (int64_t)a.max_q * d.G <= 32;
     with_type16(a.q_type, [&](auto t) {
         with_type(a.out_type, [&](auto to) {
-            launch_kernel(k_attn8_rows<decltype(t), decltype(to)>,
-                          dim3((unsigned)std::min(d.max_q * d.q_heads, 1 << 20), (unsigned)d.B), dim3(64), 0, st, d);
+            using T = decltype(t);
+            using TO = decltype(to);
+            if (few) {
+                if (d.D <= 64) launch_few<T, TO, 64, 8>(d, a, st);
+                else if (d.D <= 128) launch_few<T, TO, 128, 8>(d, a, st);
+                else launch_few<T, TO, 256, 4>(d, a, st);
+            } else {
+                if (d.D <= 64) launch_many<T, TO, 64, 64, 2>(d, a, st);
+                else if (d.D <= 128) launch_many<T, TO, 128, 64, 2>(d, a, st);
+                else launch_many<T, TO, 256, 32, 1>(d, a, st);
+            }
         });
     });
     return hipGetLastError();
