@@ -13,6 +13,8 @@
 // Rows, tiles and their order are those of the attention over 16-bit values: the
 // queries of a sequence times the G query heads of a cache head, 32 rows a wave, X^T
 // = K Q^T (keys down, rows across), O^T += V^T P^T.
+#include <utility>
+
 #include "qgemv_attn.h"
 
 namespace qgemv {
@@ -137,6 +139,26 @@ template <int DP> struct Place16 {
     static __device__ __forceinline__ int v(int r) { return DP == 64 ? (r >> 1 & 1) * 5 : (r & 3) << 2 | ((r >> 2 ^ r) & 3); }
 };
 
+// x[e] times what lane e of the lane's row of sixteen holds.
+template <int E>
+__device__ __forceinline__ float lane_of_row(float s) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x150 + E, 0xf, 0xf, true));
+}
+template <int E>
+__device__ __forceinline__ float times_lane(float x, float s) {
+    float y = lane_of_row<E>(s) * x;
+    asm("" : "+v"(y));   // (in pairs the products would not take the broadcast in)
+    return y;
+}
+template <int... E>
+__device__ __forceinline__ void times_lanes(f32x16& x, float s, std::integer_sequence<int, E...>) {
+    ((x[E] = times_lane<E>(x[E], s)), ...);
+}
+__device__ __forceinline__ void times_lanes(f32x16& x, float s) {
+    asm volatile("" : "+v"(s));   // (the broadcasts are this product's own, not shared with another's in registers)
+    times_lanes(x, s, std::make_integer_sequence<int, 16>{});
+}
+
 // What a wave holds of its 32 rows, and the steps of a tile of KT keys.
 template <int DP, int KT>
 struct Rows8 {
@@ -145,6 +167,7 @@ struct Rows8 {
     f32x16 o[ND];
     float m, l;
     int r;                       // exponent field of the scales' factor
+    float r_min;                 // the least factor of the wave's rows
     float c2;                    // what scores are multiplied by: |scale| log2(e), and q's factor
     int p, z, p_lo, p_hi, z_hi;  // place and window start of this lane's row, and of the wave's rows
                                  // (p_lo: below every key for a scale of 0, so that weights looks at every tile)
@@ -199,6 +222,7 @@ struct Rows8 {
         m = -INFINITY;
         l = 0.f;
         r = kLeast;
+        r_min = __builtin_bit_cast(float, kLeast << 23);
     }
     // X^T = K Q^T of the codes at lds + AT (JOINED), 32 dimensions a read.
     template <int AT>
@@ -232,54 +256,63 @@ struct Rows8 {
     }
     // Weights from scores, with the running maximum, sum and scale.  `there` names the
     // keys of the tile (from j0 on) that have a page, sc their scales: KT of keys, then
-    // of values.
+    // of values.  A half of the wave has sixteen of 32 keys, and each of its rows of
+    // sixteen lanes holds their scales, one a lane, which the multiplication itself
+    // broadcasts.  (Read from LDS for every lane they were a third of its traffic.)
     __device__ __forceinline__ void weights(const AttnDev& a, const float* sc, int j0, unsigned long long there,
                                             f32x16 (&x)[NX], f16x8 (&pf)[2 * NX]) {
-        const int half = (threadIdx.x & 63) >> 5;
-        f32x4v sv[NX][4];
+        const int lane = threadIdx.x & 63, half = lane >> 5, mine = 8 * (lane >> 2 & 3) + 4 * half + (lane & 3);
+        float sk[NX], sv[NX];
 #pragma unroll
-        for (int n = 0; n < NX; n++)
+        for (int n = 0; n < NX; n++) {
+            sk[n] = sc[32 * n + mine];
+            sv[n] = sc[KT + 32 * n + mine];
+        }
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const f32x4v sk = *reinterpret_cast<const f32x4v*>(sc + 32 * n + 8 * g + 4 * half);
-                sv[n][g] = *reinterpret_cast<const f32x4v*>(sc + KT + 32 * n + 8 * g + 4 * half);
-#pragma unroll
-                for (int i = 0; i < 4; i++) x[n][4 * g + i] *= sk[i];
-            }
+        for (int n = 0; n < NX; n++) times_lanes(x[n], sk[n]);
         const unsigned long long all = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
+        unsigned long long seen = ~0ull;
         if (!((there & all) == all && j0 + KT - 1 <= p_lo && (j0 >= z_hi || j0 + KT - 1 < a.sinks))) {
             if (a.scale == 0.f) {
 #pragma unroll
                 for (int n = 0; n < NX; n++) x[n] *= 0.f;
             }
-            // what the row does not see: a score of -inf, a scale of 0 (whatever they hold)
+            // the keys that this lane's row sees, from the first that the lane has on
             const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
-            const unsigned long long seen =
-                (there & below(p - j0 + 1) & (~below(z - j0) | below(a.sinks - j0))) >> (4 * half);
+            seen = (there & below(p - j0 + 1) & (~below(z - j0) | below(a.sinks - j0))) >> (4 * half);
             const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
             for (int n = 0; n < NX; n++)
 #pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const bool on = word[n] & (1u << (8 * (e / 4) + e % 4));
-                    x[n][e] = on ? x[n][e] : -INFINITY;
-                    sv[n][e / 4][e % 4] = on ? sv[n][e / 4][e % 4] : 0.f;
-                }
+                for (int e = 0; e < 16; e++)
+                    x[n][e] = word[n] & (1u << (8 * (e / 4) + e % 4)) ? x[n][e] : -INFINITY;
         }
-        float mt = x[0][0], st = sv[0][0][0];
+        float mt = x[0][0];
 #pragma unroll
         for (int n = 0; n < NX; n++)
 #pragma unroll
-            for (int e = 0; e < 16; e++) {
-                mt = fmaxf(mt, x[n][e]);
-                st = fmaxf(st, sv[n][e / 4][e % 4]);
-            }
+            for (int e = 0; e < 16; e++) mt = fmaxf(mt, x[n][e]);
         mt = max_halves(mt) * c2;
-        st = max_halves(st);
-        if (__any(mt > m + kSlack8 || st > __builtin_bit_cast(float, r << 23))) {
+        bool grows = mt > m + kSlack8;
+#pragma unroll
+        for (int n = 0; n < NX; n++) grows |= sv[n] > r_min;
+        if (__any(grows)) {
+            // (the largest scale that the row sees here; one that it does not see may be anything)
+            const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+            float st = 0.f;
+#pragma unroll
+            for (int n = 0; n < NX; n++) {
+                f32x16 f;
+#pragma unroll
+                for (int e = 0; e < 16; e++) f[e] = word[n] & (1u << (8 * (e / 4) + e % 4)) ? 1.f : 0.f;
+                // (0 * inf of an unseen scale is NaN, which the maximum passes over)
+                times_lanes(f, sv[n]);
+#pragma unroll
+                for (int e = 0; e < 16; e++) st = fmaxf(st, f[e]);
+            }
+            st = max_halves(st);
+            const int rn = min(max(r, (int)((__builtin_bit_cast(uint32_t, st) + 0x7fffffu) >> 23)), kMost);   // (up to a power of two)
             const float mn = fmaxf(m, mt);
-            const int e = (int)((__builtin_bit_cast(uint32_t, fmaxf(st, 0.f)) + 0x7fffffu) >> 23);   // (up to a power of two)
-            const int rn = min(max(r, e), kMost);
             const float fix = (mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn)) *
                               __builtin_bit_cast(float, (127 + r - rn) << 23);
             l *= fix;
@@ -287,19 +320,25 @@ struct Rows8 {
             for (int d = 0; d < ND; d++) o[d] *= fix;
             m = mn;
             r = rn;
+            int least = r;
+            for (int w = 32; w; w >>= 1) least = min(least, __shfl_xor(least, w));
+            r_min = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(least) << 23);
         }
         const float mu = m == -INFINITY ? 0.f : m - kLift8 + (float)(r - 127);
         // (l takes a tile's weights at once: one by one those below half of its last
         // bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is)
         float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < NX; n++)
+        for (int n = 0; n < NX; n++) {
 #pragma unroll
             for (int e = 0; e < 16; e++) {
-                const float w = __builtin_amdgcn_exp2f(fmaf(x[n][e], c2, -mu));
-                sum += w;
-                pf[2 * n + e / 8][e % 8] = (f16)(w * sv[n][e / 4][e % 4]);
+                x[n][e] = __builtin_amdgcn_exp2f(fmaf(x[n][e], c2, -mu));
+                sum += x[n][e];
             }
+            times_lanes(x[n], sv[n]);
+#pragma unroll
+            for (int e = 0; e < 16; e++) pf[2 * n + e / 8][e % 8] = (f16)x[n][e];
+        }
         l += sum;
     }
     // After the last tile: l with both halves' keys, and m as what a weight of 1 stands
