@@ -22,6 +22,7 @@ namespace qgemv {
 struct Attn8Dev : AttnDev {     // (strides of codes in bytes)
     const float *ks, *vs;
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    uint32_t page_bytes, slot_bytes, scale_page, scale_slot;   // the strides where `runs` holds
 };
 
 __device__ __forceinline__ int64_t scale_offset(const Attn8Dev& a, int page, int j) {
@@ -96,8 +97,12 @@ __device__ void attn8_row(const Attn8Dev& a, const Span& s, const int32_t* table
 // code's byte, its top bit turned over, in the low bits; 1152 less is the code.
 // Five instructions for four codes.
 typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) char lbyte;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// (loads that are known to be global: others count as LDS's too, which then are waited for all at once)
+typedef __attribute__((address_space(1))) const u32x4 gmem16;
+typedef __attribute__((address_space(1))) const float gmemf;
 __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi) {
     const f16x2 off = {(f16)-1152.f, (f16)-1152.f};
     const uint32_t w[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
@@ -121,6 +126,9 @@ __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
 // scales overflow and are left to attn8_row; what smaller ones add may be lost).
 constexpr float kSlack8 = 8.f, kLift8 = 7.f;
 constexpr int kLeast = 127 - 60, kMost = 127 + 60;
+
+// Kinds of instructions for the order that the scheduler is asked for.
+constexpr int kValu = 0x402, kMfma = 0x8, kDsRead = 0x100;
 
 // Where chunks of 16 bytes of a row stand: chunk c of row r of an LDS tile at place c
 // ^ f(r) of the row.  Codes (rows of DP bytes): 16 lanes that read one chunk of
@@ -154,9 +162,17 @@ template <int... E>
 __device__ __forceinline__ void times_lanes(f32x16& x, float s, std::integer_sequence<int, E...>) {
     ((x[E] = times_lane<E>(x[E], s)), ...);
 }
+template <int USE>
 __device__ __forceinline__ void times_lanes(f32x16& x, float s) {
-    asm volatile("" : "+v"(s));   // (the broadcasts are this product's own, not shared with another's in registers)
+    asm("; use %1" : "+v"(s) : "n"(USE));   // (the broadcasts are this use's own, not shared with another's in registers)
     times_lanes(x, s, std::make_integer_sequence<int, 16>{});
+}
+
+// (fmaxf would first make each of them quiet, one instruction more a value)
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
 }
 
 // What a wave holds of its 32 rows, and the steps of a tile of KT keys.
@@ -168,9 +184,10 @@ struct Rows8 {
     float m, l;
     int r;                       // exponent field of the scales' factor
     float r_min;                 // the least factor of the wave's rows
+    float mu;                    // what is taken from a score (times c2) before its exponential
     float c2;                    // what scores are multiplied by: |scale| log2(e), and q's factor
-    int p, z, p_lo, p_hi, z_hi;  // place and window start of this lane's row, and of the wave's rows
-                                 // (p_lo: below every key for a scale of 0, so that weights looks at every tile)
+    int p, z, p_lo, p_hi, z_lo, z_hi;  // place and window start of this lane's row, and of the wave's rows
+                                 // (p_lo: below every key for a scale of 0, so that scaled looks at every tile)
 
     // The rows first_row .. first_row + 31 of the block; this lane's is `row`.  A
     // lane has, of each 32 dimensions, the 16 from `first` on: in two runs of 8
@@ -183,8 +200,9 @@ struct Rows8 {
         z = window_start(a, p);
         p_lo = a.scale == 0.f ? INT32_MIN : s.place(min(first_row / a.G, s.i1));
         p_hi = s.place(min((first_row + 31) / a.G, s.i1));
+        z_lo = window_start(a, s.place(min(first_row / a.G, s.i1)));
         z_hi = window_start(a, p_hi);
-        // (the sign of the scale is moved into q; a scale of 0 is taken in weights, because
+        // (the sign of the scale is moved into q; a scale of 0 is taken in scaled, because
         // the -inf of a hidden key times 0 would be NaN)
         c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const T* q = (const T*)a.q + (int64_t)(s.s0 + qi) * a.ldq + (int64_t)hq * a.D;
@@ -240,36 +258,46 @@ struct Rows8 {
             }
         }
     }
-    // The same of halves (not JOINED).
+    // The same of halves (not JOINED).  The reads run AHEAD of the products (one by one,
+    // each waited for, they would be most of a tile's time).
     template <int AT>
     __device__ __forceinline__ void scores16(const char* lds, f32x16 (&x)[NX]) {
         const int half = (threadIdx.x & 63) >> 5, row = threadIdx.x & 31;
+        constexpr int N = NX * NS, AHEAD = 6;
+        f16x8 kf[N];
 #pragma unroll
-        for (int n = 0; n < NX; n++) {
-            x[n] = f32x16{};
-#pragma unroll
-            for (int k = 0; k < NS; k++) {
-                const char* at = lds + row * DP * 2 + ((2 * k + half) ^ Place16<DP>::k(row)) * 16;
-                x[n] = mfma(*reinterpret_cast<const f16x8*>(at + AT + 32 * n * DP * 2), qf[k], x[n]);
-            }
+        for (int i = 0; i < N; i++) {
+            const char* at = lds + row * DP * 2 + ((2 * (i / NX) + half) ^ Place16<DP>::k(row)) * 16;
+            kf[i] = *reinterpret_cast<const f16x8*>(at + AT + 32 * (i % NX) * DP * 2);
         }
+#pragma unroll
+        for (int n = 0; n < NX; n++) x[n] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < N; i++) x[i % NX] = mfma(kf[i], qf[i / NX], x[i % NX]);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, AHEAD, 0);
+#pragma unroll
+        for (int i = 0; i < N - AHEAD; i++) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kMfma, AHEAD, 0);
     }
-    // Weights from scores, with the running maximum, sum and scale.  `there` names the
-    // keys of the tile (from j0 on) that have a page, sc their scales: KT of keys, then
-    // of values.  A half of the wave has sixteen of 32 keys, and each of its rows of
+    // Scores with the keys' scales, and the running maximum and largest scale.  `there`
+    // names the keys of the tile (from j0 on) that have a page, sc their scales: KT of keys,
+    // then of values (sv: this lane's).  A half of the wave has sixteen of 32 keys, and each of its rows of
     // sixteen lanes holds their scales, one a lane, which the multiplication itself
     // broadcasts.  (Read from LDS for every lane they were a third of its traffic.)
-    __device__ __forceinline__ void weights(const AttnDev& a, const float* sc, int j0, unsigned long long there,
-                                            f32x16 (&x)[NX], f16x8 (&pf)[2 * NX]) {
+    __device__ __forceinline__ void scaled(const AttnDev& a, const float* sc, int j0, unsigned long long there,
+                                           f32x16 (&x)[NX], float (&sv)[NX]) {
         const int lane = threadIdx.x & 63, half = lane >> 5, mine = 8 * (lane >> 2 & 3) + 4 * half + (lane & 3);
-        float sk[NX], sv[NX];
+        float sk[NX];
 #pragma unroll
         for (int n = 0; n < NX; n++) {
             sk[n] = sc[32 * n + mine];
             sv[n] = sc[KT + 32 * n + mine];
         }
 #pragma unroll
-        for (int n = 0; n < NX; n++) times_lanes(x[n], sk[n]);
+        for (int n = 0; n < NX; n++) times_lanes<0>(x[n], sk[n]);
         const unsigned long long all = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
         unsigned long long seen = ~0ull;
         if (!((there & all) == all && j0 + KT - 1 <= p_lo && (j0 >= z_hi || j0 + KT - 1 < a.sinks))) {
@@ -287,11 +315,10 @@ struct Rows8 {
                 for (int e = 0; e < 16; e++)
                     x[n][e] = word[n] & (1u << (8 * (e / 4) + e % 4)) ? x[n][e] : -INFINITY;
         }
-        float mt = x[0][0];
+        float mt = max3(x[0][0], x[0][1], x[0][2]);
 #pragma unroll
-        for (int n = 0; n < NX; n++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) mt = fmaxf(mt, x[n][e]);
+        for (int e = 3; e < 16 * NX - 1; e += 2) mt = max3(mt, x[e / 16][e % 16], x[(e + 1) / 16][(e + 1) % 16]);
+        mt = max3(mt, mt, x[NX - 1][15]);
         mt = max_halves(mt) * c2;
         bool grows = mt > m + kSlack8;
 #pragma unroll
@@ -306,7 +333,7 @@ struct Rows8 {
 #pragma unroll
                 for (int e = 0; e < 16; e++) f[e] = word[n] & (1u << (8 * (e / 4) + e % 4)) ? 1.f : 0.f;
                 // (0 * inf of an unseen scale is NaN, which the maximum passes over)
-                times_lanes(f, sv[n]);
+                times_lanes<1>(f, sv[n]);
 #pragma unroll
                 for (int e = 0; e < 16; e++) st = fmaxf(st, f[e]);
             }
@@ -324,21 +351,20 @@ struct Rows8 {
             for (int w = 32; w; w >>= 1) least = min(least, __shfl_xor(least, w));
             r_min = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(least) << 23);
         }
-        const float mu = m == -INFINITY ? 0.f : m - kLift8 + (float)(r - 127);
-        // (l takes a tile's weights at once: one by one those below half of its last
-        // bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is)
+        mu = m == -INFINITY ? 0.f : m - kLift8 + (float)(r - 127);
+    }
+    // The weights of 32 keys.  (l takes them at once: one by one those below half of its
+    // last bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is.)
+    __device__ __forceinline__ void form(f32x16& x, float sv, f16x8* pf) {
         float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < NX; n++) {
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-                x[n][e] = __builtin_amdgcn_exp2f(fmaf(x[n][e], c2, -mu));
-                sum += x[n][e];
-            }
-            times_lanes(x[n], sv[n]);
-#pragma unroll
-            for (int e = 0; e < 16; e++) pf[2 * n + e / 8][e % 8] = (f16)x[n][e];
+        for (int e = 0; e < 16; e++) {
+            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c2, -mu));
+            sum += x[e];
         }
+        times_lanes<2>(x, sv);
+#pragma unroll
+        for (int e = 0; e < 16; e++) pf[e / 8][e % 8] = (f16)x[e];
         l += sum;
     }
     // After the last tile: l with both halves' keys, and m as what a weight of 1 stands
@@ -384,38 +410,54 @@ struct Rows8 {
         }
     }
     // The same of halves: keys 8 w + 4 half .. + 3 of sixteen a read.
-    __device__ __forceinline__ static uint32_t v_part16(const char* lds, int d, int w) {
+    __device__ __forceinline__ static const lmem* v_part16(const char* lds, int d, int w) {
         const int lane = threadIdx.x & 63, half = lane >> 5, g = lane >> 4, i = lane & 15;
         const int key = 8 * w + 4 * half + (i >> 2);
         const int chunk = 4 * d + 2 * (g & 1) + ((i & 3) >> 1);
-        return (uint32_t)(uintptr_t)(lmem*)(lds + key * DP * 2 + (chunk ^ Place16<DP>::v(key)) * 16 + (i & 1) * 8);
+        return (const lmem*)(lds + key * DP * 2 + (chunk ^ Place16<DP>::v(key)) * 16 + (i & 1) * 8);
+    }
+    // The weights of a tile and O^T += V^T P^T of the halves at lds + AT.  V's reads run
+    // ahead, and the weights of the second 32 keys are formed beside the products of the
+    // first.
+    template <int AT>
+    __device__ __forceinline__ void read16(const char* lds, int u, f16x8 (&v)[ND]) {
+#pragma unroll
+        for (int d = 0; d < ND; d++) {
+            union { s16x4 w[2]; f16x8 v; } f;
+#pragma unroll
+            for (int w = 0; w < 2; w++)
+                f.w[w] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lmem4*)((lbyte*)v_part16(lds, d, w) + (AT + u * 16 * DP * 2)));
+            v[d] = f.v;
+        }
     }
     template <int AT>
-    __device__ __forceinline__ void add16(const char* lds, const f16x8 (&pf)[2 * NX]) {
-        static_assert(AT + KT * DP * 2 <= 65536, "offsets of a read");
-        two_steps16<AT, 0>(lds, pf);
-        if constexpr (NX == 2) two_steps16<AT, 2>(lds, pf);
-    }
-    template <int AT, int U>
-    __device__ __forceinline__ void two_steps16(const char* lds, const f16x8 (&pf)[2 * NX]) {
+    __device__ __forceinline__ void add16(const char* lds, f32x16 (&x)[NX], const float (&sv)[NX]) {
+        f16x8 pf[2 * NX], v[2][ND];
+        auto step = [&](int u) {
 #pragma unroll
-        for (int d = 0; d < ND; d += 2) {
-            s16x4 v[2][2][2];   // [step][dimensions][eight keys]
-            asm volatile(
-                "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
-                "ds_read_b64_tr_b16 %2, %10 offset:%12\n\tds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
-                "ds_read_b64_tr_b16 %4, %8 offset:%13\n\tds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
-                "ds_read_b64_tr_b16 %6, %10 offset:%13\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(v[0][0][0]), "=&v"(v[0][0][1]), "=&v"(v[0][1][0]), "=&v"(v[0][1][1]),
-                  "=&v"(v[1][0][0]), "=&v"(v[1][0][1]), "=&v"(v[1][1][0]), "=&v"(v[1][1][1])
-                : "v"(v_part16(lds, d, 0)), "v"(v_part16(lds, d, 1)), "v"(v_part16(lds, d + 1, 0)),
-                  "v"(v_part16(lds, d + 1, 1)), "n"(AT + U * 16 * DP * 2), "n"(AT + (U + 1) * 16 * DP * 2)
-                : "memory");
+            for (int d = 0; d < ND; d++) o[d] = mfma(v[u % 2][d], pf[u], o[d]);
+        };
+        read16<AT>(lds, 0, v[0]);
+        form(x[0], sv[0], pf);
+        __builtin_amdgcn_sched_barrier(0);
+        read16<AT>(lds, 1, v[1]);
+        step(0);
+        if constexpr (NX == 2) {
+            read16<AT>(lds, 2, v[0]);
+            step(1);
+            form(x[1], sv[1], pf + 2);
 #pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) o[d + c] = mfma(__builtin_bit_cast(f16x8, v[u][c]), pf[U + u], o[d + c]);
+            for (int i = 0; i < 2 * ND; i++) {
+                __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(kValu, 80 / (2 * ND), 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            read16<AT>(lds, 3, v[1]);
+            step(2);
+            step(3);
+        } else {
+            step(1);
         }
     }
 };
@@ -426,10 +468,11 @@ __device__ const uint4 g_zeros8[QGEMV_HEAD_DIM_MAX / 16] = {};
 // The pages of a tile's keys, from 64 columns of the table at a time (one a
 // lane): a tile's columns are within 64 even with a page for every key.  A tile
 // whose keys are all there, in pages of whole runs of 16 (a.runs), is addressed
-// by scalars: one page and one base a run.  Any other has an offset for every
-// key.
+// by scalars, one page and one offset a run, with products of 32 bits.  Any other
+// has an offset for every key.
 template <int DP, int KT>
 struct Pages8 {
+    static constexpr int CPR = DP / 16, RPI = 64 / CPR;   // chunks of a row; rows of a wave's load of 1 KB
     int first = -64, page = -1;            // the lane's column is first + lane
     unsigned long long valid = 0;          // columns with a page of the pool
     int j0;                                // the tile: its first key
@@ -457,7 +500,7 @@ struct Pages8 {
         }
         const unsigned long long need = (2ull << (c1 - c0)) - 1;
         runs = a.runs && j0 + KT <= s.limit && (valid >> (c0 - first) & need) == need;
-        if (runs) return ~0ull;
+        if (__builtin_expect(runs, 1)) return ~0ull;
         const int key = j0 + (KT == 64 ? lane : lane & (KT - 1));
         const int c = a.page_shift >= 0 ? key >> a.page_shift : key / a.page_size;
         const int mine = __shfl(page, c - first);
@@ -467,62 +510,27 @@ struct Pages8 {
         }
         return __ballot(off >= 0);
     }
-    __device__ __forceinline__ int run_page(const AttnDev& a, int key) const {
-        return __builtin_amdgcn_readlane(page, (key >> a.page_shift) - first);
+    // Row `row` of the tile, the first or another of (part of) a run: its page, and where
+    // it is.
+    __device__ __forceinline__ uint32_t run_page(const AttnDev& a, int row) const {
+        return __builtin_amdgcn_readlane(page, ((j0 + row) >> a.page_shift) - first);
     }
-
-    // Where this lane's 16 codes of COUNT loads of the tile's K or V are, from row row0
-    // on, 1 KB of rows a load: f(load, address).  `swizzle` says which chunk of its row a
-    // lane takes.
-    template <int COUNT, typename S, typename F>
-    __device__ __forceinline__ void walk(const AttnDev& a, const char* from, int row0, S swizzle, F f) const {
-        constexpr int CPR = DP / 16, RPI = 64 / CPR;
-        if (__builtin_expect(runs, 1)) {
-            const int lane = threadIdx.x & 63, lr = lane / CPR, lc = lane % CPR;
-            constexpr int RUN = COUNT * RPI < 16 ? COUNT : 16 / RPI;   // loads of (part of) a run
-            static_assert(COUNT % RUN == 0, "whole runs");
-            const uint32_t stride = (uint32_t)a.token_stride;
-#pragma unroll
-            for (int r = 0; r < COUNT / RUN; r++) {
-                const int key = j0 + row0 + RUN * RPI * r;
-                const char* base = from + (run_page(a, key) * a.page_stride + (key & (a.page_size - 1)) * a.token_stride);
-#pragma unroll
-                for (int c = 0; c < RUN; c++) {
-                    const int row = row0 + RUN * RPI * r + RPI * c;
-                    uint32_t at = (RPI * c + lr) * stride + 16 * (lc ^ swizzle(row | lr));
-                    asm volatile("" : "+v"(at));   // (32 bits to keep, not an address)
-                    f(RUN * r + c, base + at);
-                }
-            }
-            return;
-        }
-        // (hidden from the compiler, which would form addresses for this branch
-        // ahead of the loop over tiles, in registers that the others need)
-        int lane = threadIdx.x & 63;
-        asm volatile("" : "+v"(lane));
-        const int lr = lane / CPR, lc = lane % CPR;
-#pragma unroll
-        for (int c = 0; c < COUNT; c++) {
-            const int row = row0 + RPI * c + lr;
-            const int64_t at = __shfl((long long)off, row);
-            const int chunk = lc ^ swizzle(row);
-            const char* g = from + (at + 16 * chunk);
-            f(c, at >= 0 && 16 * chunk < a.D ? g : (const char*)g_zeros8);
-        }
+    __device__ __forceinline__ uint64_t run(const Attn8Dev& a, int row) const {
+        return (uint64_t)run_page(a, row) * a.page_bytes + (uint32_t)((j0 + row) & (a.page_size - 1)) * a.slot_bytes;
     }
-    // Where the scale of key `row` of the tile is (of the array `from`, at its head's).
+    // Where chunk `chunk` of the tile's row `row` is, of a tile that has no runs (of an
+    // address, which may be nobody's, and `from`, the head's).
+    __device__ __forceinline__ const char* single(const AttnDev& a, const char* from, int row, int chunk) const {
+        const int64_t at = __shfl((long long)off, row);
+        return at >= 0 && 16 * chunk < a.D ? from + at + 16 * chunk : (const char*)g_zeros8;
+    }
+    // Where the scale of the tile's row `row` is.
     __device__ __forceinline__ const float* scale(const Attn8Dev& a, const float* from, int row) const {
         if (__builtin_expect(runs, 1)) {
-            const float* base[KT / 16];
+            uint32_t pg = run_page(a, 0);
 #pragma unroll
-            for (int u = 0; u < KT / 16; u++) {
-                const int key = j0 + 16 * u;
-                base[u] = from + (run_page(a, key) * a.scale_page_stride + (key & (a.page_size - 1)) * a.scale_token_stride);
-            }
-            const float* b = base[0];
-#pragma unroll
-            for (int u = 1; u < KT / 16; u++) b = row / 16 == u ? base[u] : b;
-            return b + (uint32_t)(row & 15) * (uint32_t)a.scale_token_stride;
+            for (int u = 1; u < KT / 16; u++) pg = row >= 16 * u ? run_page(a, 16 * u) : pg;
+            return from + ((uint64_t)pg * a.scale_page + (uint32_t)((j0 + row) & (a.page_size - 1)) * a.scale_slot);
         }
         const int64_t at = __shfl((long long)soff, row);
         return at >= 0 ? from + at : (const float*)g_zeros8;
@@ -543,7 +551,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     constexpr int TILE = KT * DP * 2, BUF = 2 * TILE;    // bytes of a K (or V) tile, and of both
     constexpr int LOADS = KT / RPI / NW;                 // wave loads of K (and of V) per wave
     constexpr int SC = 2 * KT;                           // scales of a tile
-    static_assert(LOADS >= 1 && KT <= 64 && SC <= 64 * NW, "tile shape");
+    static_assert(LOADS >= 1 && KT <= 64 && SC <= 64 * NW && SC % 64 == 0, "tile shape");
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     float* sc = reinterpret_cast<float*>(lds + 2 * BUF);
 
@@ -575,15 +583,27 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     const float* sbase = (threadIdx.x < KT ? a.ks : a.vs) + h * a.scale_head_stride;
     u32x4 kc[LOADS], vc[LOADS];
     float scale;
-    const auto plain = [](int) { return 0; };
     auto ask_tile = [&](int t) -> unsigned long long {
         const unsigned long long there = pages.tile(a, s, table, tile_of(s, t) * KT);
-        pages.template walk<LOADS>(a, kbase, RPI * LOADS * wave, plain,
-                                   [&](int c, const char* g) { kc[c] = *reinterpret_cast<const u32x4*>(g); });
-        pages.template walk<LOADS>(a, vbase, RPI * LOADS * wave, plain,
-                                   [&](int c, const char* g) { vc[c] = *reinterpret_cast<const u32x4*>(g); });
-        const float* g = pages.scale(a, sbase, threadIdx.x & (KT - 1));
-        if (threadIdx.x < SC) scale = *g;
+        constexpr int MINE = RPI * LOADS;    // rows of the tile that this wave takes, in one run
+        static_assert(16 % MINE == 0, "rows of a wave");
+        if (__builtin_expect(pages.runs, 1)) {
+            const uint64_t run = pages.run(a, MINE * wave);
+            const uint32_t at = (lane / CPR) * a.slot_bytes + 16 * (lane % CPR);
+#pragma unroll
+            for (int c = 0; c < LOADS; c++) {
+                kc[c] = *(gmem16*)(kbase + run + (at + RPI * c * a.slot_bytes));
+                vc[c] = *(gmem16*)(vbase + run + (at + RPI * c * a.slot_bytes));
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < LOADS; c++) {
+                const int row = MINE * wave + RPI * c + lane / CPR;
+                kc[c] = *(gmem16*)pages.single(a, kbase, row, lane % CPR);
+                vc[c] = *(gmem16*)pages.single(a, vbase, row, lane % CPR);
+            }
+        }
+        if (wave < SC / 64) scale = *(gmemf*)pages.scale(a, sbase, threadIdx.x & (KT - 1));
         return there;
     };
     // (a row's chunk c of 16 codes becomes its chunks 2 c and 2 c + 1 of eight halves)
@@ -599,7 +619,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
             *reinterpret_cast<f16x8*>(v + (chunk ^ Place16<DP>::v(row)) * 16) = halves(vc[c][0], vc[c][1]);
             *reinterpret_cast<f16x8*>(v + (chunk + 1 ^ Place16<DP>::v(row)) * 16) = halves(vc[c][2], vc[c][3]);
         }
-        if (threadIdx.x < SC) sc[buf * SC + threadIdx.x] = scale;
+        if (wave < SC / 64) sc[buf * SC + threadIdx.x] = scale;
     };
 
     unsigned long long there = 0, there_next = 0;
@@ -612,12 +632,12 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
         constexpr int AT = buf * BUF;
         if (t + 1 < s.t1) there_next = ask_tile(t + 1);
         const int j0 = tile_of(s, t) * KT;
-        if (active && j0 <= w.p_hi && (j0 + KT > window_start(a, w.p_lo) || j0 < a.sinks)) {
+        if (active && j0 <= w.p_hi && (j0 + KT > w.z_lo || j0 < a.sinks)) {
             f32x16 x[R::NX];
-            f16x8 pf[2 * R::NX];
+            float sv[R::NX];
             w.template scores16<AT>(lds, x);
-            w.weights(a, sc + buf * SC, j0, there, x, pf);
-            w.template add16<AT + TILE>(lds, pf);
+            w.scaled(a, sc + buf * SC, j0, there, x, sv);
+            w.template add16<AT + TILE>(lds, x, sv);
         }
         if (t + 1 < s.t1) put_tile(1 - buf);
         __syncthreads();
@@ -682,7 +702,7 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     constexpr int KT = 32, ROWS = 32;
     typedef Rows8<DP, KT> R;
     constexpr int TILE = KT * DP, SCB = 2 * KT * 4, RING = 4 * TILE + 2 * SCB;   // K, K, V, V, scales, scales
-    constexpr int RPI = 64 / (DP / 16), LOADS = KT / RPI;                       // wave loads of a tile
+    constexpr int CPR = DP / 16, RPI = 64 / CPR, LOADS = KT / RPI;             // wave loads of a tile
     extern __shared__ __attribute__((aligned(1024))) char lds[];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -703,15 +723,29 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     const int each = (s.t1 - s.t0 + NW - 1) / NW;
     const int t0 = min(s.t0 + wave * each, s.t1), t1 = min(t0 + each, s.t1);
     auto take = [&](int t) { return pages.tile(a, s, table, tile_of(s, t) * KT); };
+    // one wave load of 1 KB after another, a lane's chunk of a row by the chunk's place
+    auto load = [&](const char* from, char* to, auto place) {
+        if (__builtin_expect(pages.runs, 1)) {
+            constexpr int PER = RPI < 16 ? 16 / RPI : 1;     // loads of a run
+#pragma unroll
+            for (int c = 0; c < LOADS; c++) {
+                const char* base = from + pages.run(a, 16 * (c / PER));
+                const int row = RPI * (c % PER) + lane / CPR;
+                to_lds16(base + (row * a.slot_bytes + 16 * (lane % CPR ^ place(row))), to + 1024 * c);
+            }
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < LOADS; c++) {
+            const int row = RPI * c + lane / CPR;
+            to_lds16(pages.single(a, from, row, lane % CPR ^ place(row)), to + 1024 * c);
+        }
+    };
     auto load_k = [&](int slot) {
-        char* to = mine + slot * TILE;
-        pages.template walk<LOADS>(a, kbase, 0, Place8<DP>::k, [&](int c, const char* g) { to_lds16(g, to + 1024 * c); });
+        load(kbase, mine + slot * TILE, Place8<DP>::k);
         __builtin_amdgcn_global_load_lds((gmem*)pages.scale(a, sbase, row32), (lmem*)(mine + 4 * TILE + slot * SCB), 4, 0, 0);
     };
-    auto load_v = [&](int slot) {
-        char* to = mine + (2 + slot) * TILE;
-        pages.template walk<LOADS>(a, vbase, 0, Place8<DP>::v, [&](int c, const char* g) { to_lds16(g, to + 1024 * c); });
-    };
+    auto load_v = [&](int slot) { load(vbase, mine + (2 + slot) * TILE, Place8<DP>::v); };
     if (t0 < t1) {
         unsigned long long there[2];
 #pragma unroll
@@ -724,13 +758,13 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
         auto step = [&](int t, auto at) {
             constexpr int SLOT = at;
             f32x16 x[R::NX];
-            f16x8 pf[2 * R::NX];
+            float sv[R::NX];
             // (loads land in their order: K S V of this tile, K S V of the next, K S of the one after)
             const int left = t1 - 1 - t;
             if (left > 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * LOADS + 1) : "memory");
             else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
             w.template scores8<SLOT * TILE>(mine, x);
-            w.weights(a, reinterpret_cast<const float*>(mine + 4 * TILE + SLOT * SCB), tile_of(s, t) * KT, there[0], x, pf);
+            w.scaled(a, reinterpret_cast<const float*>(mine + 4 * TILE + SLOT * SCB), tile_of(s, t) * KT, there[0], x, sv);
             QGEMV_WAIT("lgkmcnt(0)");
             there[0] = there[1];
             if (left > 1) {
@@ -742,6 +776,9 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
             } else {
                 QGEMV_WAIT("vmcnt(0)");
             }
+            f16x8 pf[2 * R::NX];
+#pragma unroll
+            for (int n = 0; n < R::NX; n++) w.form(x[n], sv[n], pf + 2 * n);
             w.template add8<(2 + SLOT) * TILE>(mine, pf);
             QGEMV_WAIT("lgkmcnt(0)");
             if (left > 1) load_v(SLOT);
@@ -793,10 +830,10 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     }
 }
 
-template <typename T, typename TO, int DP, int KT, int OCC>
+template <typename T, typename TO, int DP, int KT, int OCC, int NW>
 static void launch_many(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
-    constexpr int NW = 4, ROWS = 32 * NW;
-    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC, DP == 64 ? 1024 : 0, a.ws_bytes, a.ws);
+    constexpr int ROWS = 32 * NW;
+    split(d, a.max_kv, ROWS, KT, 4, 256 * OCC * 4 / NW, DP == 64 ? 1024 : 0, a.ws_bytes, a.ws);
     launch_kernel(k_attn8_many<T, TO, DP, KT, NW, OCC>,
                   dim3((unsigned)(d.heads * d.splits * d.row_tiles), (unsigned)d.B), dim3(64 * NW),
                   2 * (2 * KT * DP * 2 + 2 * KT * 4), st, d);
@@ -824,8 +861,12 @@ hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st) {
     d.D = a.c.head_dim; d.B = a.B; d.max_q = a.max_q; d.n_pages = a.c.n_pages;
     d.page_size = a.c.page_size; d.window = a.window; d.sinks = a.sinks; d.scale = a.scale;
     d.page_shift = (a.c.page_size & (a.c.page_size - 1)) == 0 ? __builtin_ctz(a.c.page_size) : -1;
-    d.runs = (d.D == 64 || d.D == 128 || d.D == 256) && d.page_shift >= 4 && d.token_stride < (1 << 26) &&
-             d.scale_token_stride < (1 << 26);
+    constexpr int64_t k31 = (int64_t)1 << 31;
+    d.runs = (d.D == 64 || d.D == 128 || d.D == 256) && d.page_shift >= 4 && d.page_stride < k31 &&
+             d.scale_page_stride < k31 && d.token_stride < k31 && d.token_stride * d.page_size < k31 &&
+             d.scale_token_stride < k31 && d.scale_token_stride * d.page_size < k31;
+    d.page_bytes = (uint32_t)d.page_stride; d.slot_bytes = (uint32_t)d.token_stride;
+    d.scale_page = (uint32_t)d.scale_page_stride; d.scale_slot = (uint32_t)d.scale_token_stride;
     const bool few = (int64_t)a.max_q * d.G <= 32;
     with_type16(a.q_type, [&](auto t) {
         with_type(a.out_type, [&](auto to) {
@@ -836,9 +877,9 @@ hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st) {
                 else if (d.D <= 128) launch_few<T, TO, 128, 8>(d, a, st);
                 else launch_few<T, TO, 256, 4>(d, a, st);
             } else {
-                if (d.D <= 64) launch_many<T, TO, 64, 64, 2>(d, a, st);
-                else if (d.D <= 128) launch_many<T, TO, 128, 64, 2>(d, a, st);
-                else launch_many<T, TO, 256, 32, 1>(d, a, st);
+                if (d.D <= 64) launch_many<T, TO, 64, 64, 2, 4>(d, a, st);
+                else if (d.D <= 128) launch_many<T, TO, 128, 64, 2, 8>(d, a, st);
+                else launch_many<T, TO, 256, 32, 1, 4>(d, a, st);
             }
         });
     });
