@@ -22,6 +22,7 @@ namespace qgemv {
 struct Attn8Dev : AttnDev {     // (strides of codes in bytes)
     const float *ks, *vs;
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    bool by_die;
     uint32_t page_bytes, slot_bytes, scale_page, scale_slot;   // the strides where `runs` holds
 };
 
@@ -707,7 +708,16 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, row32 = lane & 31;
-    const int h = blockIdx.x % a.heads, part = blockIdx.x / a.heads, b = blockIdx.y;
+    // Workgroups go round the eight dies in turn.  A line of scales has a few keys of
+    // several heads, so the heads of a part of a sequence run on one die and share it in
+    // its L2.
+    int h = blockIdx.x % a.heads, group = blockIdx.x / a.heads + a.splits * blockIdx.y;
+    if (a.by_die) {
+        h = blockIdx.x / 8;
+        group = blockIdx.x % 8 + 8 * blockIdx.y;
+    }
+    const int b = group / a.splits, part = group - b * a.splits;
+    if (b >= a.B) return;
     const int32_t* table = a.table + b * a.ldt;
     Pages8<DP, KT> pages;
     Span s;
@@ -842,7 +852,10 @@ static void launch_many(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
 template <typename T, typename TO, int DP, int NW>
 static void launch_few(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
     split(d, a.max_kv, 32, 32, 4 * NW, 256, 0, a.ws_bytes, a.ws);
-    launch_kernel(k_attn8_few<T, TO, DP, NW>, dim3((unsigned)(d.heads * d.splits), (unsigned)d.B),
+    const int64_t groups = (int64_t)d.B * d.splits;
+    d.by_die = groups >= 8;
+    launch_kernel(k_attn8_few<T, TO, DP, NW>,
+                  d.by_die ? dim3(8u * d.heads, (unsigned)((groups + 7) / 8)) : dim3((unsigned)(d.heads * d.splits), (unsigned)d.B),
                   dim3(64 * NW), NW * (4 * 32 * DP + 512 + 256), st, d);
     join<TO, 32, 32, DP / 4>(d, st);
 }
