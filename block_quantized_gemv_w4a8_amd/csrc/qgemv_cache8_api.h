@@ -192,9 +192,9 @@ qgemv_status qgemv_verify_draft(const void* logits, int logits_type, int64_t T, 
                     (long long)ldl, (long long)ldd);
     if (!type_any(logits_type))
         return fail(QGEMV_E_UNSUPPORTED, "%s: logits_type %d", name, logits_type);
-    if (T > (1 << 28) || V > (1 << 24) || B > 65535 || max_q > 65535)
+    if (T > (1 << 28) || V > (1 << 22) || B > 65535 || max_q > 65535)
         return fail(QGEMV_E_UNSUPPORTED,
-                    "%s: T above 2^28, V above 2^24, or B or max_q above 65535", name);
+                    "%s: T above 2^28, V above 2^22, or B or max_q above 65535", name);
     if (!aligned(logits, type_bytes(logits_type)) || (draft && !aligned(draft, 4)))
         return fail(QGEMV_E_ALIGN, "%s: logits and draft must be aligned to their elements", name);
     if (!aligned(q_start, 4) || !aligned(tokens, 4) || !aligned(u, 4) ||

@@ -611,7 +611,7 @@ qgemv_status qgemv_cache_read_q8(const qgemv_kv_cache_q8* cache, int64_t T, cons
  *      tokens were certain: probability 1 for tokens[r], 0 for others.
  *   temperature: fp32 [B], or NULL for 1.  accepted, next: int32 [B].
  *   ws: as for qgemv_paged_attn; without enough a sequence is one workgroup's work.
- * Limits: T at most 2^28, V at most 2^24, B and max_q at most 65535. */
+ * Limits: T at most 2^28, V at most 2^22, B and max_q at most 65535. */
 qgemv_status qgemv_verify_draft(const void* logits, int logits_type, int64_t T, int64_t V,
                                 int64_t ldl, const int32_t* q_start, int B, int max_q,
                                 const int32_t* tokens, const float* draft, int64_t ldd,
