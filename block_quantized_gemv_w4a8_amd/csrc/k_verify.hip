@@ -13,13 +13,12 @@
 // and sum (joined with exp((m - M) / t)), so that sums over chunks give the chunk in
 // which the border lies and only that one is walked value by value.
 //
-// Two launches: the chunks of all rows; then, for each sequence, what is accepted
-// (found again by every workgroup: a few loads) and the sums of what a refused
-// draft leaves of each chunk, after which the workgroup that comes last draws.
-// Sums are taken in the order of their places, so the order of arrival changes
-// nothing.  Bound by the logits' bytes: the 64-bit exponential of a value, 18
-// instructions, takes about 0.7 of the time that its four bytes do.
+// Three launches: the chunks of all rows; for each sequence what is accepted (found
+// again by every workgroup: a few loads) and the sums of what a refused draft leaves of
+// each chunk; the draw.  (With the draw left to the workgroup that comes last, the
+// releases of memory that this takes made the second launch 31 us of 84.)
 #include <algorithm>
+#include <type_traits>
 
 #include "qgemv_layer.h"
 
@@ -39,6 +38,19 @@ struct ChunkStat {
     int at;
 };
 
+// What a row's chunks say together: its largest value, first at `best`, and the sum.
+struct RowStat {
+    double inv;      // 1 / sum, 0 where there is no mass
+    float top;
+    int best;
+};
+// What the second launch found of a sequence: the row that the next token comes from,
+// `done` rows on.
+struct Choice {
+    RowStat row;
+    int done;
+};
+
 struct VerifyDev {
     const void* logits;
     const int32_t *q_start, *tokens;
@@ -46,16 +58,40 @@ struct VerifyDev {
     int32_t *accepted, *next;
     ChunkStat* stats;     // [B][max_q][chunks]
     double* left;         // [B][chunks]
-    int* arrived;         // [B]
+    Choice* choice;       // [B]
     int64_t ldl, ldd;
     int T, V, B, max_q, chunks;
+};
+
+// 2^z for z <= 0 (0 for NaN) from the Taylor series of 2^f about 0, |f| <= 1/2 what is
+// left of z beside a whole number: the first term left out is (f ln 2)^11 / 11! < 2^-42.
+// The coefficients are kept in registers (of scalars each step would copy one first).
+struct Series {
+    double c[11];
+    __device__ __forceinline__ Series() {
+        constexpr double L = 0.6931471805599453;
+        c[0] = 1.0;
+#pragma unroll
+        for (int i = 1; i < 11; i++) c[i] = c[i - 1] * L / i;
+#pragma unroll
+        for (int i = 0; i < 11; i++) asm volatile("" : "+v"(c[i]));
+    }
+    __device__ __forceinline__ double power(double z) const {
+        z = fmax(z, -1100.0);
+        const double n = rint(z), f = z - n;
+        double p = c[10];
+#pragma unroll
+        for (int i = 9; i >= 0; i--) p = fma(p, f, c[i]);
+        return ldexp(p, (int)n);
+    }
 };
 
 // The rows of sequence b, and its temperature.
 struct Seq {
     int s0, n;
     bool greedy;
-    double inv;      // 1 / temperature
+    double inv;      // log2(e) / temperature
+    Series series;
 };
 __device__ __forceinline__ Seq sequence(const VerifyDev& a, int b) {
     Seq s;
@@ -63,30 +99,15 @@ __device__ __forceinline__ Seq sequence(const VerifyDev& a, int b) {
     s.n = min(min(max(a.q_start[b + 1], s.s0), a.T) - s.s0, a.max_q);
     const float t = a.temperature ? a.temperature[b] : 1.f;
     s.greedy = !(t > 0.f);
-    s.inv = 1.0 / (double)t;
+    s.inv = 1.4426950408889634 / (double)t;
     return s;
 }
 
-// exp(y) for y <= 0 from the Taylor series about 0 of what is left of y beside n
-// ln 2, |r| <= 0.347: the first term left out is r^13 / 13! < 2^-52.
-__device__ __forceinline__ double exponential(double y) {
-    y = fmax(y, -800.0);
-    const double n = rint(y * 1.4426950408889634);
-    const double r = fma(n, 1.7239444525614835e-13, fma(n, -0.6931471805601177, y));   // (ln 2 as 40 bits and the rest: n times the first is exact)
-    double p = 1.0 / 479001600.0;
-    constexpr double inv[12] = {1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0,
-                                1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
-#pragma unroll
-    for (int i = 0; i < 12; i++) p = fma(p, r, inv[i]);
-    return ldexp(p, (int)n);
-}
 // e of a logit against the largest, top (not -inf): a -inf has none whatever the
-// temperature, and where top is +inf the largest share the mass.
-__device__ __forceinline__ double mass(float x, float top, double inv) {
-    const double d = (double)x - (double)top;
-    return x == top ? 1.0 : d == -INFINITY ? 0.0 : exponential(d * inv);
-}
-__device__ __forceinline__ float real(float x) { return x == x ? x : -INFINITY; }
+// temperature (-inf * 0 is NaN).
+__device__ __forceinline__ double mass(float x, float top, const Seq& s) { return s.series.power(((double)x - (double)top) * s.inv); }
+// A logit as it counts: -inf for NaN, the largest number for +inf.
+__device__ __forceinline__ float real(float x) { return x == x ? fminf(x, 3.402823466e38f) : -INFINITY; }
 template <typename T>
 __device__ __forceinline__ float logit(const T* row, int v) {
     return real((float)row[v]);
@@ -132,11 +153,9 @@ __device__ __forceinline__ int wave_min(int x) {
     return over_wave(x, [](int p, int q) { return min(p, q); });
 }
 
-// One chunk of a row, by a wave.
+// One chunk of a row, by a wave that has its values.
 template <typename T>
-__device__ __forceinline__ ChunkStat chunk_stat(const VerifyDev& a, const T* row, int c, const Seq& s) {
-    float x[VPL];
-    chunk_values(row, a.V, c, -INFINITY, x);
+__device__ __forceinline__ ChunkStat chunk_stat(float (&x)[VPL], int c, const Seq& s) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; i++) {
@@ -155,50 +174,69 @@ __device__ __forceinline__ ChunkStat chunk_stat(const VerifyDev& a, const T* row
     }
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; i++) sum += mass(x[i], top, s.inv);
+    for (int i = 0; i < VPL; i++) sum += mass(x[i], top, s);
     r.sum = wave_sum(sum);
     return r;
 }
 
-// What a row's chunks say together: its largest value, first at `best`, and the sum.
-struct RowStat {
-    double sum;
-    float top;
-    int best;
-};
-__device__ __forceinline__ double chunk_mass(const ChunkStat& c, float top, double inv) {
-    return c.sum > 0.0 ? c.sum * mass(c.top, top, inv) : 0.0;
+__device__ __forceinline__ double chunk_mass(const ChunkStat& c, float top, const Seq& s) {
+    return c.sum > 0.0 ? c.sum * mass(c.top, top, s) : 0.0;
 }
-// (by a wave)
+// (by a wave, which has up to HELD chunks a lane at hand and reads the others twice)
 __device__ RowStat row_stat(const ChunkStat* stats, int chunks, const Seq& s) {
+    constexpr int HELD = 3;
     const int lane = threadIdx.x & 63;
+    ChunkStat held[HELD];
     float top = -INFINITY;
-    for (int c = lane; c < chunks; c += 64) top = fmaxf(top, stats[c].top);
+#pragma unroll
+    for (int i = 0; i < HELD; i++) {
+        held[i] = ChunkStat{0.0, -INFINITY, 0};
+        if (lane + 64 * i < chunks) held[i] = stats[lane + 64 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < HELD; i++) top = fmaxf(top, held[i].top);
+    for (int c = lane + 64 * HELD; c < chunks; c += 64) top = fmaxf(top, stats[c].top);
     top = wave_max(top);
     RowStat r{0.0, top, -1};
     if (top == -INFINITY) return r;
     if (s.greedy) {
         int at = INT32_MAX;
-        for (int c = lane; c < chunks; c += 64)
+#pragma unroll
+        for (int i = 0; i < HELD; i++)
+            if (held[i].top == top) at = min(at, held[i].at);
+        for (int c = lane + 64 * HELD; c < chunks; c += 64)
             if (stats[c].top == top) at = min(at, stats[c].at);
         r.best = wave_min(at);
         return r;
     }
     double sum = 0.0;
-    for (int c = lane; c < chunks; c += 64) sum += chunk_mass(stats[c], top, s.inv);
-    r.sum = wave_sum(sum);
+#pragma unroll
+    for (int i = 0; i < HELD; i++) sum += chunk_mass(held[i], top, s);
+    for (int c = lane + 64 * HELD; c < chunks; c += 64) sum += chunk_mass(stats[c], top, s);
+    r.inv = 1.0 / wave_sum(sum);
     return r;
 }
-// p of a logit of a row that has mass, and of one of its values.
-__device__ __forceinline__ double prob(float x, const RowStat& r, const Seq& s) { return mass(x, r.top, s.inv) / r.sum; }
+// p of a logit.
+__device__ __forceinline__ double prob(float x, const RowStat& r, const Seq& s) { return mass(x, r.top, s) * r.inv; }
+
+// What the acceptance of the draft behind a row takes, asked for ahead of the row's sum.
+struct Draft {
+    int token;     // -1: none that can be accepted
+    float x, q, u;
+};
 template <typename T>
-__device__ __forceinline__ bool passes(const VerifyDev& a, int row, const RowStat& r, const Seq& s) {
-    const int token = a.tokens[row + 1];
-    if (token < 0 || token >= a.V) return false;
-    const float q = a.draft ? a.draft[(int64_t)(row + 1) * a.ldd + token] : 1.f;
-    const double p = s.greedy ? (token == r.best ? 1.0 : 0.0)
-                              : r.sum > 0.0 ? prob(logit((const T*)a.logits + (int64_t)row * a.ldl, token), r, s) : 0.0;
-    return (double)a.u[row + 1] * (q > 0.f ? (double)q : 0.0) < p;
+__device__ __forceinline__ Draft draft_of(const VerifyDev& a, int row) {
+    Draft d{a.tokens[row + 1], 0.f, 1.f, a.u[row + 1]};
+    if (d.token < 0 || d.token >= a.V) d.token = -1;
+    if (d.token < 0) return d;
+    d.x = logit((const T*)a.logits + (int64_t)row * a.ldl, d.token);
+    if (a.draft) d.q = a.draft[(int64_t)(row + 1) * a.ldd + d.token];
+    return d;
+}
+__device__ __forceinline__ bool passes(const Draft& d, const RowStat& r, const Seq& s) {
+    if (d.token < 0 || r.top == -INFINITY) return false;
+    const double p = s.greedy ? (d.token == r.best ? 1.0 : 0.0) : prob(d.x, r, s);
+    return (double)d.u * (d.q > 0.f ? (double)d.q : 0.0) < p;
 }
 
 // The weights that the next token is drawn by: p, or what the draft leaves of it.
@@ -323,8 +361,8 @@ __device__ int drawn(const VerifyDev& a, Kind kind, int row, float u, const RowS
 template <typename T>
 __device__ int drawn_whole(const VerifyDev& a, bool refused, int row, float u, const RowStat& r, const Seq& s, const ChunkStat* stats) {
     __shared__ double rest;
-    if (!(r.sum > 0.0)) return -1;
-    const auto whole = [&](int c) { return chunk_mass(stats[c], r.top, s.inv) / r.sum; };
+    if (!(r.inv > 0.0)) return -1;
+    const auto whole = [&](int c) { return chunk_mass(stats[c], r.top, s) * r.inv; };
     if (refused && !a.draft) {
         const int token = a.tokens[row + 1], its = token >= 0 && token < a.V ? token / VCH : -1;
         if (threadIdx.x < 64 && its >= 0) {
@@ -338,36 +376,49 @@ __device__ int drawn_whole(const VerifyDev& a, bool refused, int row, float u, c
     return drawn<T>(a, kWhole, row, u, r, s, whole);
 }
 
-// The chunks of all rows, a wave each.
-template <typename T>
+// The chunks of all rows, PER a wave, the next on its way while one is summed.
+template <typename T, int PER>
 __global__ __launch_bounds__(VWG) void k_verify_stats(const VerifyDev a) {
-    const int c = blockIdx.x * VWAVES + (threadIdx.x >> 6), i = blockIdx.y, b = blockIdx.z;
-    if (blockIdx.x == 0 && i == 0 && threadIdx.x == 0) a.arrived[b] = 0;
+    const int c0 = (blockIdx.x * VWAVES + (threadIdx.x >> 6)) * PER, i = blockIdx.y, b = blockIdx.z;
     const Seq s = sequence(a, b);
-    if (i >= s.n || c >= a.chunks) return;
-    const ChunkStat r = chunk_stat(a, (const T*)a.logits + (int64_t)(s.s0 + i) * a.ldl, c, s);
-    if ((threadIdx.x & 63) == 0) a.stats[((int64_t)b * a.max_q + i) * a.chunks + c] = r;
+    if (i >= s.n || c0 >= a.chunks) return;
+    const T* row = (const T*)a.logits + (int64_t)(s.s0 + i) * a.ldl;
+    ChunkStat* to = a.stats + ((int64_t)b * a.max_q + i) * a.chunks;
+    float x[2][VPL];
+    chunk_values(row, a.V, c0, -INFINITY, x[0]);
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int c = c0 + k;
+        if (c >= a.chunks) break;
+        if (k + 1 < PER && c + 1 < a.chunks) chunk_values(row, a.V, c + 1, -INFINITY, x[(k + 1) % 2]);
+        const ChunkStat r = chunk_stat<T>(x[k % 2], c, s);
+        if ((threadIdx.x & 63) == 0) to[c] = r;
+    }
 }
 
-// What is accepted, and the next token.
-template <typename T>
-__global__ __launch_bounds__(VWG) void k_verify_pick(const VerifyDev a) {
-    __shared__ int stop, last;
+// What is accepted, and the sums of what a refused draft leaves of each chunk, PER a wave.
+template <typename T, int PER>
+__global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
+    __shared__ int stop;
     __shared__ RowStat at;
-    __shared__ double sums[VWAVES];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.y;
     const Seq s = sequence(a, b);
     const ChunkStat* stats = a.stats + (int64_t)b * a.max_q * a.chunks;
     // the first row whose draft is refused, four rows at a time: the last row has none
-    if (threadIdx.x == 0) stop = s.n > 0 ? s.n - 1 : 0;
+    if (threadIdx.x == 0) {
+        stop = s.n > 0 ? s.n - 1 : 0;
+        at = RowStat{0.0, -INFINITY, -1};
+    }
     __syncthreads();
     for (int i0 = 0; i0 < s.n; i0 += VWAVES) {
         const int i = i0 + wave;
         RowStat r{};
         bool ends = false;
         if (i < s.n) {
+            Draft d{};
+            if (i + 1 < s.n) d = draft_of<T>(a, s.s0 + i);
             r = row_stat(stats + (int64_t)i * a.chunks, a.chunks, s);
-            ends = i + 1 == s.n || !passes<T>(a, s.s0 + i, r, s);
+            ends = i + 1 == s.n || !passes(d, r, s);
         }
         if (ends && lane == 0) atomicMin(&stop, i);
         __syncthreads();
@@ -376,37 +427,39 @@ __global__ __launch_bounds__(VWG) void k_verify_pick(const VerifyDev a) {
         __syncthreads();
         if (now < i0 + VWAVES) break;
     }
-    const int done = stop, row = s.s0 + done;
+    const int done = stop;
     const RowStat r = at;
-    const bool refused = s.n > 0 && done + 1 < s.n;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.choice[b] = Choice{r, done};
+    if (s.n == 0 || s.greedy || done + 1 >= s.n || !a.draft || !(r.inv > 0.0)) return;
+    const int c0 = (blockIdx.x * VWAVES + wave) * PER;
+    for (int c = c0; c < min(c0 + PER, a.chunks); c++) {
+        const double w = chunk_weight<T>(a, kLeft, s.s0 + done, c, r, s);
+        if (lane == 0) a.left[(int64_t)b * a.chunks + c] = w;
+    }
+}
+
+// The next token.
+template <typename T>
+__global__ __launch_bounds__(VWG) void k_verify_draw(const VerifyDev a) {
+    const int b = blockIdx.x;
+    const Seq s = sequence(a, b);
+    const Choice pick = a.choice[b];
+    const int row = s.s0 + pick.done;
+    const bool refused = pick.done + 1 < s.n;
     int next = -1;
-    if (s.n > 0 && !s.greedy && refused && a.draft && r.sum > 0.0) {
-        const int c = blockIdx.x * VWAVES + wave;
-        if (c < a.chunks) {
-            const double w = chunk_weight<T>(a, kLeft, row, c, r, s);
-            if (lane == 0) sums[wave] = w;
+    if (s.n > 0 && s.greedy) {
+        next = pick.row.best;
+    } else if (s.n > 0 && pick.row.inv > 0.0) {
+        const float u = a.u[s.s0];
+        if (refused && a.draft) {
+            const double* left = a.left + (int64_t)b * a.chunks;
+            next = drawn<T>(a, kLeft, row, u, pick.row, s, [&](int c) { return left[c]; });
         }
-        __syncthreads();
-        double* left = a.left + (int64_t)b * a.chunks;
-        if (threadIdx.x == 0) {
-            for (int w = 0; w < VWAVES; w++) {
-                const int cc = blockIdx.x * VWAVES + w;
-                if (cc < a.chunks) __hip_atomic_store(left + cc, sums[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-            last = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
-        }
-        __syncthreads();
-        if (!last) return;
-        next = drawn<T>(a, kLeft, row, a.u[s.s0], r, s,
-                        [&](int cc) { return __hip_atomic_load(left + cc, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); });
-        if (next < 0) next = drawn_whole<T>(a, false, row, a.u[s.s0], r, s, stats + (int64_t)done * a.chunks);
-    } else {
-        if (blockIdx.x != 0) return;
-        if (s.n > 0)
-            next = s.greedy ? r.best : drawn_whole<T>(a, refused, row, a.u[s.s0], r, s, stats + (int64_t)done * a.chunks);
+        if (next < 0)
+            next = drawn_whole<T>(a, refused, row, u, pick.row, s, a.stats + ((int64_t)b * a.max_q + pick.done) * a.chunks);
     }
     if (threadIdx.x == 0) {
-        a.accepted[b] = done;
+        a.accepted[b] = pick.done;
         a.next[b] = next;
     }
 }
@@ -424,13 +477,15 @@ __global__ __launch_bounds__(VWG) void k_verify_one(const VerifyDev a) {
         const int row = s.s0 + i;
         __syncthreads();
         for (int c = wave; c < a.chunks; c += VWAVES) {
-            const ChunkStat st = chunk_stat(a, (const T*)a.logits + (int64_t)row * a.ldl, c, s);
+            float x[VPL];
+            chunk_values((const T*)a.logits + (int64_t)row * a.ldl, a.V, c, -INFINITY, x);
+            const ChunkStat st = chunk_stat<T>(x, c, s);
             if (lane == 0) stats[c] = st;
         }
         __syncthreads();
         const RowStat r = row_stat(stats, a.chunks, s);
         const bool refused = i + 1 < s.n;
-        if (refused && passes<T>(a, row, r, s)) {
+        if (refused && passes(draft_of<T>(a, row), r, s)) {
             done++;
             continue;
         }
@@ -439,7 +494,7 @@ __global__ __launch_bounds__(VWG) void k_verify_one(const VerifyDev a) {
             break;
         }
         const float u = a.u[s.s0];
-        if (refused && a.draft && r.sum > 0.0) {
+        if (refused && a.draft && r.inv > 0.0) {
             for (int c = wave; c < a.chunks; c += VWAVES) {
                 const double w = chunk_weight<T>(a, kLeft, row, c, r, s);
                 if (lane == 0) sums[c] = w;
@@ -463,21 +518,31 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
     d.ldl = a.ldl; d.ldd = a.ldd;
     d.T = (int)a.T; d.V = (int)a.V; d.B = a.B; d.max_q = a.max_q;
     d.chunks = (int)((a.V + VCH - 1) / VCH);
-    // the workspace: how many workgroups of a sequence have come, what drafts leave of
-    // each chunk, and the chunks of all rows
-    const int64_t count = ((int64_t)d.B * 4 + 15) / 16 * 16, left = ((int64_t)d.B * d.chunks * 8 + 15) / 16 * 16;
+    // the workspace: what is chosen of each sequence, what drafts leave of each chunk, and
+    // the chunks of all rows
+    const int64_t choice = ((int64_t)d.B * sizeof(Choice) + 15) / 16 * 16, left = ((int64_t)d.B * d.chunks * 8 + 15) / 16 * 16;
     const int64_t rows = (int64_t)d.B * d.max_q;
     const int64_t most = std::min<int64_t>(a.ws_bytes, QGEMV_WS_BYTES);
-    const bool fits = rows > 0 && count + left <= most && rows <= (most - count - left) / (d.chunks * (int64_t)sizeof(ChunkStat));
-    d.arrived = (int*)a.ws;
-    d.left = (double*)((char*)a.ws + count);
-    d.stats = (ChunkStat*)((char*)a.ws + count + left);
+    const bool fits = rows > 0 && choice + left <= most && rows <= (most - choice - left) / (d.chunks * (int64_t)sizeof(ChunkStat));
+    d.choice = (Choice*)a.ws;
+    d.left = (double*)((char*)a.ws + choice);
+    d.stats = (ChunkStat*)((char*)a.ws + choice + left);
     with_type(a.logits_type, [&](auto t) {
         using T = decltype(t);
         if (fits && (int64_t)d.chunks * d.max_q > kOne) {
-            const unsigned x = (unsigned)((d.chunks + VWAVES - 1) / VWAVES);
-            launch_kernel(k_verify_stats<T>, dim3(x, (unsigned)d.max_q, (unsigned)d.B), dim3(VWG), 0, st, d);
-            launch_kernel(k_verify_pick<T>, dim3(x, (unsigned)d.B), dim3(VWG), 0, st, d);
+            const auto go = [&](auto per, bool last) {
+                constexpr int PER = decltype(per)::value;
+                const unsigned x = (unsigned)((d.chunks + VWAVES * PER - 1) / (VWAVES * PER));
+                if (last) launch_kernel(k_verify_left<T, PER>, dim3(x, (unsigned)d.B), dim3(VWG), 0, st, d);
+                else launch_kernel(k_verify_stats<T, PER>, dim3(x, (unsigned)d.max_q, (unsigned)d.B), dim3(VWG), 0, st, d);
+            };
+            const auto one = std::integral_constant<int, 1>{};
+            const auto four = std::integral_constant<int, 4>{};
+            if (rows * d.chunks <= 8192) go(one, false);
+            else go(four, false);
+            if ((int64_t)d.B * d.chunks <= 4096) go(one, true);
+            else go(four, true);
+            launch_kernel(k_verify_draw<T>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
         } else {
             launch_kernel(k_verify_one<T>, dim3((unsigned)a.B), dim3(VWG),
                           (unsigned)(d.chunks * (sizeof(ChunkStat) + sizeof(double))), st, d);

@@ -597,9 +597,9 @@ qgemv_status qgemv_cache_read_q8(const qgemv_kv_cache_q8* cache, int64_t T, cons
  * accepted tokens and the next one are then distributed as tokens drawn from p.
  * Exponentials and sums are 64-bit.
  *   A temperature that is not above 0 means p_r = 1 at the first of the largest logits
- *   and 0 elsewhere.  A logit of -inf or NaN has p = 0 (of +inf: all of the mass, shared
- *   among its like); a row without any other has no mass: nothing is accepted
- *   from it and next[b] = -1.  A draft probability that is not above 0 (or NaN) is 0.
+ *   and 0 elsewhere.  A logit of -inf or NaN has p = 0 (+inf counts as the largest
+ *   fp32 number); a row without any other has no mass: nothing is accepted from it
+ *   and next[b] = -1.  A draft probability that is not above 0 (or NaN) is 0.
  *   A sequence without rows gets accepted = 0 and next = -1.
  *   logits: [T][ldl] of logits_type, V values a row, aligned to their elements.
  *   q_start: int32 [B + 1], held to [0, T]; max_q: at least the most rows of a
