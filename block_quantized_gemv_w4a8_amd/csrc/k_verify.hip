@@ -28,7 +28,6 @@ constexpr int VWG = 256;           // threads of a workgroup
 constexpr int VWAVES = VWG / 64;
 constexpr int VPL = 16;            // values of a chunk a lane
 constexpr int VCH = 64 * VPL;      // values of a chunk
-constexpr int kOne = 0;            // chunks of a sequence that one workgroup takes by itself
 
 // A chunk of a row: sum of e against its own largest value, which is first at `at`
 // (looked for only where the temperature is 0).
@@ -63,26 +62,42 @@ struct VerifyDev {
     int T, V, B, max_q, chunks;
 };
 
-// 2^z for z <= 0 (0 for NaN) from the Taylor series of 2^f about 0, |f| <= 1/2 what is
-// left of z beside a whole number: the first term left out is (f ln 2)^11 / 11! < 2^-42.
-// The coefficients are kept in registers (of scalars each step would copy one first).
+// 2^z for z <= 0 (0 for NaN): 2^f, |f| <= 1/2 what is left of z beside a whole number n,
+// as 1 + f g(f) with g of degree 8 interpolated at Chebyshev's points (off by 4e-14, exact
+// at 0).  The coefficients are kept in registers (of scalars each step would copy one
+// first).
 struct Series {
-    double c[11];
+    double c[9];
     __device__ __forceinline__ Series() {
-        constexpr double L = 0.6931471805599453;
-        c[0] = 1.0;
+        constexpr double g[9] = {0.6931471805599453, 0.2402265069581299, 0.055504108664760424, 0.009618129159402558,
+                                 0.0013333558179043112, 0.00015403455852453838, 1.525268684626772e-05, 1.3255224878668817e-06,
+                                 1.0203121063391729e-07};
 #pragma unroll
-        for (int i = 1; i < 11; i++) c[i] = c[i - 1] * L / i;
+        for (int i = 0; i < 9; i++) {
+            c[i] = g[i];
+            asm volatile("" : "+v"(c[i]));
+        }
+    }
+    __device__ __forceinline__ double part(double f) const {
+        double p = c[8];
 #pragma unroll
-        for (int i = 0; i < 11; i++) asm volatile("" : "+v"(c[i]));
+        for (int i = 7; i >= 0; i--) p = fma(p, f, c[i]);
+        return fma(p, f, 1.0);
     }
     __device__ __forceinline__ double power(double z) const {
         z = fmax(z, -1100.0);
-        const double n = rint(z), f = z - n;
-        double p = c[10];
-#pragma unroll
-        for (int i = 9; i >= 0; i--) p = fma(p, f, c[i]);
-        return ldexp(p, (int)n);
+        const double n = rint(z);
+        return ldexp(part(z - n), (int)n);
+    }
+    // The same but for 2^-1000 where that is less: n is left in the low bits of a sum, and
+    // added to the exponent.  (For sums over a row, whose largest is 1: instructions of the
+    // full rate only.)
+    __device__ __forceinline__ double above(double z) const {
+        constexpr double kWhole = 6755399441055744.0;   // 1.5 * 2^52
+        z = fmax(z, -1000.0);
+        const double t = z + kWhole;
+        const double p = part(z - (t - kWhole));
+        return __hiloint2double(__double2hiint(p) + (__double2loint(t) << 20), __double2loint(p));
     }
 };
 
@@ -156,13 +171,16 @@ __device__ __forceinline__ int wave_min(int x) {
 // One chunk of a row, by a wave that has its values.
 template <typename T>
 __device__ __forceinline__ ChunkStat chunk_stat(float (&x)[VPL], int c, const Seq& s) {
+    // (the maximum passes over NaN, and above() takes a NaN as the least)
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        x[i] = real(x[i]);
-        top = fmaxf(top, x[i]);
-    }
+    for (int i = 0; i < VPL; i++) top = fmaxf(top, x[i]);
     top = wave_max(top);
+    if (top == INFINITY) {
+        top = real(top);
+#pragma unroll
+        for (int i = 0; i < VPL; i++) x[i] = real(x[i]);
+    }
     ChunkStat r{0.0, top, 0};
     if (top == -INFINITY) return r;
     if (s.greedy) {
@@ -174,7 +192,7 @@ __device__ __forceinline__ ChunkStat chunk_stat(float (&x)[VPL], int c, const Se
     }
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; i++) sum += mass(x[i], top, s);
+    for (int i = 0; i < VPL; i++) sum += s.series.above(((double)x[i] - (double)top) * s.inv);
     r.sum = wave_sum(sum);
     return r;
 }
@@ -529,7 +547,9 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
     d.stats = (ChunkStat*)((char*)a.ws + choice + left);
     with_type(a.logits_type, [&](auto t) {
         using T = decltype(t);
-        if (fits && (int64_t)d.chunks * d.max_q > kOne) {
+        // (few chunks of few sequences: one workgroup each.  4 rows of 2000 values take 11.7 us, by
+        // three launches 14.3; of 10000 values 19.4 and 14.5; 8 sequences of 4 rows of 600 15.9 and 15.5)
+        if (fits && ((int64_t)d.chunks * d.max_q > 16 || d.B > 4)) {
             const auto go = [&](auto per, bool last) {
                 constexpr int PER = decltype(per)::value;
                 const unsigned x = (unsigned)((d.chunks + VWAVES * PER - 1) / (VWAVES * PER));
@@ -538,9 +558,8 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
             };
             const auto one = std::integral_constant<int, 1>{};
             const auto four = std::integral_constant<int, 4>{};
-            if (rows * d.chunks <= 8192) go(one, false);
-            else go(four, false);
-            if ((int64_t)d.B * d.chunks <= 4096) go(one, true);
+            go(one, false);
+            if ((int64_t)d.B * d.chunks <= 8192) go(one, true);
             else go(four, true);
             launch_kernel(k_verify_draw<T>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
         } else {

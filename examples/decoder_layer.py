@@ -1,5 +1,6 @@
 """One decoder layer over a paged cache, with int8 weights: a prompt in chunks,
-then single tokens of a ragged batch.
+then single tokens of a ragged batch, over a cache in 16 or in 8 bits; and tokens
+drafted ahead and verified.
 
     python examples/decoder_layer.py
 
@@ -33,12 +34,18 @@ class Weight:
 
 
 class Cache:
-    """Pools of pages for keys and values, and the table of pages of each sequence."""
+    """Pools of pages for keys and values, in bf16 or in int8 codes with a scale a row, and
+    the table of pages of each sequence."""
 
-    def __init__(self, pages, page, sequences, heads, dim, longest):
-        self.page = page
-        self.k, self.v = (torch.zeros(pages, page, heads, dim, dtype=torch.bfloat16, device=DEV) for _ in range(2))
-        self.pools = qg.kv_cache(self.k, self.v)
+    def __init__(self, pages, page, sequences, heads, dim, longest, bits=16):
+        self.page, self.bits = page, bits
+        kind = torch.bfloat16 if bits == 16 else torch.int8
+        self.k, self.v = (torch.zeros(pages, page, heads, dim, dtype=kind, device=DEV) for _ in range(2))
+        if bits == 16:
+            self.pools = qg.kv_cache(self.k, self.v)
+        else:
+            self.k_scale, self.v_scale = (torch.zeros(pages, page, heads, device=DEV) for _ in range(2))
+            self.pools = qg.kv_cache_q8(self.k, self.v, self.k_scale, self.v_scale)
         self.free = list(range(pages))
         self.lengths = [0] * sequences
         self.table = torch.full((sequences, -(-longest // page)), -1, dtype=torch.int32)
@@ -52,6 +59,14 @@ class Cache:
             slots.append(int(self.table[sequence, j // self.page]) * self.page + j % self.page)
         self.lengths[sequence] += tokens
         return slots
+
+    def cut(self, sequence, tokens):
+        """A sequence's last tokens given up; its pages without any are free again."""
+        self.lengths[sequence] -= tokens
+        for c in range(-(-self.lengths[sequence] // self.page), self.table.shape[1]):
+            if self.table[sequence, c] >= 0:
+                self.free.append(int(self.table[sequence, c]))
+                self.table[sequence, c] = -1
 
 
 class Batch:
@@ -96,10 +111,16 @@ class Layer:
         q = torch.empty(b.T, h, dtype=torch.bfloat16, device=DEV)
         out = torch.empty(b.T, h, device=DEV)
         ld = qkv.stride(0)
-        qg.qgemv_rope_append(cache.pools, b.T, qg.QGEMV_TYPE_F32, qkv, ld, self.heads, qkv[:, h:], ld, qkv[:, h + n:], ld, b.pos, b.slots,
-                             self.inv_freq, D, qg.QGEMV_ROPE_HALVES, q, h)
-        qg.qgemv_paged_attn(cache.pools, q, b.T, h, self.heads, b.start, b.kv_len, b.B, b.max_q, b.max_kv, b.table, b.table.shape[1],
-                            D**-0.5, self.window, self.sinks, out, qg.QGEMV_TYPE_F32, h, None, self.ws, qg.QGEMV_WS_BYTES)
+        rope = (b.pos, b.slots, self.inv_freq, D, qg.QGEMV_ROPE_HALVES, q)
+        rows = (b.start, b.kv_len, b.B, b.max_q, b.max_kv, b.table, b.table.shape[1], D**-0.5, self.window, self.sinks, out, qg.QGEMV_TYPE_F32, h,
+                None, self.ws, qg.QGEMV_WS_BYTES)
+        parts = (b.T, qg.QGEMV_TYPE_F32, qkv, ld, self.heads, qkv[:, h:], ld, qkv[:, h + n:], ld)
+        if cache.bits == 16:
+            qg.qgemv_rope_append(cache.pools, *parts, *rope, h)
+            qg.qgemv_paged_attn(cache.pools, q, b.T, h, self.heads, *rows)
+        else:
+            qg.qgemv_rope_append_q8(cache.pools, *parts, *rope, qg.QGEMV_TYPE_BF16, h)
+            qg.qgemv_paged_attn_q8(cache.pools, q, qg.QGEMV_TYPE_BF16, b.T, h, self.heads, *rows)
         return out
 
     def forward(self, cache, b, x):
@@ -137,13 +158,13 @@ def norm(x):
     return x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6)
 
 
-def run(layer, lengths, chunk, single, page=16, seed=1):
+def run(layer, lengths, chunk, single, page=16, seed=1, bits=16):
     """Sequences of `lengths` tokens: prompts in chunks, the last `single` tokens one by one.
     Returns the inputs and the layer's outputs, sequence by sequence."""
     g = torch.Generator(device=DEV).manual_seed(seed)
     x = [torch.randn(n, layer.hidden, generator=g, device=DEV) for n in lengths]
     y = [[] for _ in lengths]
-    cache = Cache(sum(-(-n // page) for n in lengths) + 1, page, len(lengths), layer.kv_heads, layer.dim, max(lengths))
+    cache = Cache(sum(-(-n // page) for n in lengths) + 1, page, len(lengths), layer.kv_heads, layer.dim, max(lengths), bits)
     while any(done < n for done, n in zip(cache.lengths, lengths)):
         at = list(cache.lengths)
         counts = [min(chunk, n - single - a) if a < n - single else min(1, n - a) for a, n in zip(at, lengths)]
@@ -154,14 +175,61 @@ def run(layer, lengths, chunk, single, page=16, seed=1):
     return x, [torch.cat(p) for p in y]
 
 
+class Model:
+    """Tokens in, logits out: an embedding, one layer and a head, over a cache of its own."""
+
+    def __init__(self, layer, vocabulary, sequences, longest, page=16, bits=8, seed=2):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.layer, self.V = layer, vocabulary
+        self.embedding = torch.randn(vocabulary, layer.hidden, generator=g, device=DEV)
+        self.head = torch.randn(vocabulary, layer.hidden, generator=g, device=DEV) * 4 / layer.hidden**0.5
+        self.cache = Cache(sequences * -(-longest // page), page, sequences, layer.kv_heads, layer.dim, longest, bits)
+
+    def step(self, tokens):
+        """Lists of new tokens, one a sequence -> (logits [T, V], the batch, all tokens [T])."""
+        ids = torch.tensor([t for s in tokens for t in s], dtype=torch.int32, device=DEV)
+        b = Batch(self.cache, [len(s) for s in tokens])
+        return norm(self.layer.forward(self.cache, b, self.embedding[ids.long()])) @ self.head.t(), b, ids
+
+
+def generate(model, prompts, new, guess, temperature=0.0, seed=3):
+    """`new` tokens or more behind each prompt; guess(sequence, tokens so far) drafts what may
+    follow, for certain (no probabilities of its own).  Returns all tokens and the steps taken."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    text = [list(p) for p in prompts]
+    model.step([p[:-1] for p in prompts])
+    steps = 0
+    while min(len(t) - len(p) for t, p in zip(text, prompts)) < new:
+        drafts = [guess(s, t) for s, t in enumerate(text)]
+        logits, b, ids = model.step([[t[-1], *d] for t, d in zip(text, drafts)])
+        u = torch.rand(b.T, generator=g, device=DEV)
+        warm = torch.full((b.B,), float(temperature), device=DEV)
+        accepted, following = (torch.empty(b.B, dtype=torch.int32, device=DEV) for _ in range(2))
+        qg.qgemv_verify_draft(logits, qg.QGEMV_TYPE_F32, b.T, model.V, model.V, b.start, b.B, b.max_q, ids, None, 0, u, warm, accepted, following,
+                              model.layer.ws, qg.QGEMV_WS_BYTES)
+        for s, (a, n) in enumerate(zip(accepted.tolist(), following.tolist())):
+            model.cache.cut(s, len(drafts[s]) - a)
+            text[s] += drafts[s][:a] + [n]
+        steps += 1
+    return text, steps
+
+
 def main():
-    for window, sinks in ((0, 0), (64, 4)):
-        layer = Layer(window=window, sinks=sinks)
-        x, y = run(layer, [300, 17, 129], chunk=100, single=9)
-        for s, (a, b) in enumerate(zip(x, y)):
-            ref = layer.plain(a)
-            print(f"window {window} sinks {sinks} sequence {s}: {len(a)} tokens, relative error "
-                  f"{float((b - ref).norm() / (ref - a).norm()):.4f} of the layer's change")
+    for bits in (16, 8):
+        for window, sinks in ((0, 0), (64, 4)):
+            layer = Layer(window=window, sinks=sinks)
+            x, y = run(layer, [300, 17, 129], chunk=100, single=9, bits=bits)
+            for s, (a, b) in enumerate(zip(x, y)):
+                ref = layer.plain(a)
+                print(f"cache of {bits} bits, window {window} sinks {sinks} sequence {s}: {len(a)} tokens, relative error "
+                      f"{float((b - ref).norm() / (ref - a).norm()):.4f} of the layer's change")
+    layer, prompts = Layer(), [[1, 2, 3], [40, 50, 60, 70, 80]]
+    plain, steps = generate(Model(layer, 1000, 2, 200), prompts, 40, lambda s, t: [])
+    print(f"40 tokens one by one: {steps} steps")
+    # drafts that are right but for every sixth token
+    text, steps = generate(Model(layer, 1000, 2, 200), prompts, 40,
+                           lambda s, t: [(v + 1) % 1000 if i % 6 == 5 else v for i, v in enumerate(plain[s])][len(t):len(t) + 4])
+    print(f"with four drafts: {steps} steps, {'the same' if all(a[:43] == b[:43] for a, b in zip(text, plain)) else 'other'} tokens")
 
 
 if __name__ == "__main__":
