@@ -98,7 +98,7 @@ __device__ void attn8_row(const Attn8Dev& a, const Span& s, const int32_t* table
 // code's byte, its top bit turned over, in the low bits; 1152 less is the code.
 // Five instructions for four codes.
 typedef f16 f16x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) char lbyte;
+typedef __attribute__((address_space(3))) const f16x8 lmem16;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // (loads that are known to be global: others count as LDS's too, which then are waited for all at once)
@@ -243,34 +243,63 @@ struct Rows8 {
         r = kLeast;
         r_min = __builtin_bit_cast(float, kLeast << 23);
     }
-    // X^T = K Q^T of the codes at lds + AT (JOINED), 32 dimensions a read.
+    // X^T = K Q^T of the codes at lds + AT (JOINED), 32 dimensions a read, all reads first.
     template <int AT>
     __device__ __forceinline__ void scores8(const char* lds, f32x16 (&x)[NX]) {
         const int half = (threadIdx.x & 63) >> 5, row = threadIdx.x & 31;
+        static_assert(NX == 1, "one run of 32 keys");
+        constexpr int READS = NS / 2 < 4 ? NS / 2 : 4;
+        u32x4 c[NS / 2];
+        x[0] = f32x16{};
 #pragma unroll
-        for (int n = 0; n < NX; n++) {
-            x[n] = f32x16{};
+        for (int k = 0; k < NS / 2; k++) {
+            const char* at = lds + row * DP + ((2 * k + half) ^ Place8<DP>::k(row)) * 16;
+            c[k] = *reinterpret_cast<const u32x4*>(at + AT);
+        }
 #pragma unroll
-            for (int k = 0; k < NS / 2; k++) {
-                const char* at = lds + row * DP + ((2 * k + half) ^ Place8<DP>::k(row)) * 16;
-                const u32x4 c = *reinterpret_cast<const u32x4*>(at + AT + 32 * n * DP);
-                x[n] = mfma(halves(c[0], c[1]), qf[2 * k], x[n]);
-                x[n] = mfma(halves(c[2], c[3]), qf[2 * k + 1], x[n]);
-            }
+        for (int k = 0; k < NS / 2; k++) {
+            x[0] = mfma(halves(c[k][0], c[k][1]), qf[2 * k], x[0]);
+            x[0] = mfma(halves(c[k][2], c[k][3]), qf[2 * k + 1], x[0]);
+        }
+        __builtin_amdgcn_sched_group_barrier(kDsRead, READS, 0);
+#pragma unroll
+        for (int k = 0; k < NS / 2; k++) {
+            __builtin_amdgcn_sched_group_barrier(kValu, 20, 0);
+            __builtin_amdgcn_sched_group_barrier(kMfma, 2, 0);
+            if (k + READS < NS / 2) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
         }
     }
+    // Where in LDS this lane reads a tile of halves, formed once (the compiler would form
+    // them again for every tile): of K chunk 2 k + half of key `lane & 31`, of V keys 8 w + 4
+    // half .. + 3 of sixteen and dimensions 32 d .. + 31 by the transposing read.
+    struct Places {
+        uint32_t k[NS], v[ND][2];
+        __device__ __forceinline__ explicit Places(const char* lds) {
+            const uint32_t base = (uint32_t)(uintptr_t)(lmem*)lds;
+            const int lane = threadIdx.x & 63, half = lane >> 5, row = lane & 31, g = lane >> 4 & 1, i = lane & 15;
+#pragma unroll
+            for (int c = 0; c < NS; c++) {
+                k[c] = base + row * DP * 2 + ((2 * c + half) ^ Place16<DP>::k(row)) * 16;
+                asm volatile("" : "+v"(k[c]));
+            }
+#pragma unroll
+            for (int d = 0; d < ND; d++)
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    const int key = 8 * w + 4 * half + (i >> 2), chunk = 4 * d + 2 * g + ((i & 3) >> 1);
+                    v[d][w] = base + key * DP * 2 + (chunk ^ Place16<DP>::v(key)) * 16 + (i & 1) * 8;
+                    asm volatile("" : "+v"(v[d][w]));
+                }
+        }
+    };
     // The same of halves (not JOINED).  The reads run AHEAD of the products (one by one,
     // each waited for, they would be most of a tile's time).
     template <int AT>
-    __device__ __forceinline__ void scores16(const char* lds, f32x16 (&x)[NX]) {
-        const int half = (threadIdx.x & 63) >> 5, row = threadIdx.x & 31;
+    __device__ __forceinline__ void scores16(const Places& places, f32x16 (&x)[NX]) {
         constexpr int N = NX * NS, AHEAD = 6;
         f16x8 kf[N];
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            const char* at = lds + row * DP * 2 + ((2 * (i / NX) + half) ^ Place16<DP>::k(row)) * 16;
-            kf[i] = *reinterpret_cast<const f16x8*>(at + AT + 32 * (i % NX) * DP * 2);
-        }
+        for (int i = 0; i < N; i++) kf[i] = *(lmem16*)(uintptr_t)(places.k[i / NX] + (AT + 32 * (i % NX) * DP * 2));
 #pragma unroll
         for (int n = 0; n < NX; n++) x[n] = f32x16{};
 #pragma unroll
@@ -385,7 +414,7 @@ struct Rows8 {
     }
     // O^T += V^T P^T of the codes at lds + AT, 16 keys a step.  Other tiles are on their
     // way to LDS meanwhile, and the compiler would wait for all of them before the reads'
-    // builtin; so two steps of 64 dimensions are read, and waited for, at once.
+    // builtin; so two steps of 128 dimensions are read, and waited for, at once.
     template <int AT>
     __device__ __forceinline__ void add8(const char* lds, const f16x8 (&pf)[2 * NX]) {
         static_assert(AT + KT * DP <= 65536, "offsets of a read");
@@ -394,57 +423,64 @@ struct Rows8 {
     }
     template <int AT, int U>
     __device__ __forceinline__ void two_steps8(const char* lds, const f16x8 (&pf)[2 * NX]) {
+        constexpr int W = ND < 4 ? 2 : 4;   // runs of 32 dimensions that are read at once
 #pragma unroll
-        for (int d = 0; d < ND; d += 2) {
-            u32x2 v[2][2];   // [step][dimensions]
-            asm volatile(
-                "ds_read_b64_tr_b8 %0, %4 offset:%6\n\tds_read_b64_tr_b8 %1, %5 offset:%6\n\t"
-                "ds_read_b64_tr_b8 %2, %4 offset:%7\n\tds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
-                "s_waitcnt lgkmcnt(0)"
-                : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
-                : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
-                : "memory");
+        for (int d = 0; d < ND; d += W) {
+            u32x2 v[2][W];   // [step][dimensions]
+            if constexpr (W == 2)
+                asm volatile(
+                    "ds_read_b64_tr_b8 %0, %4 offset:%6\n\tds_read_b64_tr_b8 %1, %5 offset:%6\n\t"
+                    "ds_read_b64_tr_b8 %2, %4 offset:%7\n\tds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
+                    "s_waitcnt lgkmcnt(0)"
+                    : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
+                    : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
+                    : "memory");
+            else
+                asm volatile(
+                    "ds_read_b64_tr_b8 %0, %8 offset:%12\n\tds_read_b64_tr_b8 %1, %9 offset:%12\n\t"
+                    "ds_read_b64_tr_b8 %2, %10 offset:%12\n\tds_read_b64_tr_b8 %3, %11 offset:%12\n\t"
+                    "ds_read_b64_tr_b8 %4, %8 offset:%13\n\tds_read_b64_tr_b8 %5, %9 offset:%13\n\t"
+                    "ds_read_b64_tr_b8 %6, %10 offset:%13\n\tds_read_b64_tr_b8 %7, %11 offset:%13\n\t"
+                    "s_waitcnt lgkmcnt(0)"
+                    : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][W - 2]), "=&v"(v[0][W - 1]), "=&v"(v[1][0]), "=&v"(v[1][1]),
+                      "=&v"(v[1][W - 2]), "=&v"(v[1][W - 1])
+                    : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "v"(v_part8(lds, d + 2)), "v"(v_part8(lds, d + 3)),
+                      "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
+                    : "memory");
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int c = 0; c < 2; c++) o[d + c] = mfma(halves(v[u][c][0], v[u][c][1]), pf[U + u], o[d + c]);
+                for (int c = 0; c < W; c++) o[d + c] = mfma(halves(v[u][c][0], v[u][c][1]), pf[U + u], o[d + c]);
         }
-    }
-    // The same of halves: keys 8 w + 4 half .. + 3 of sixteen a read.
-    __device__ __forceinline__ static const lmem* v_part16(const char* lds, int d, int w) {
-        const int lane = threadIdx.x & 63, half = lane >> 5, g = lane >> 4, i = lane & 15;
-        const int key = 8 * w + 4 * half + (i >> 2);
-        const int chunk = 4 * d + 2 * (g & 1) + ((i & 3) >> 1);
-        return (const lmem*)(lds + key * DP * 2 + (chunk ^ Place16<DP>::v(key)) * 16 + (i & 1) * 8);
     }
     // The weights of a tile and O^T += V^T P^T of the halves at lds + AT.  V's reads run
     // ahead, and the weights of the second 32 keys are formed beside the products of the
     // first.
     template <int AT>
-    __device__ __forceinline__ void read16(const char* lds, int u, f16x8 (&v)[ND]) {
+    __device__ __forceinline__ void read16(const Places& places, int u, f16x8 (&v)[ND]) {
 #pragma unroll
         for (int d = 0; d < ND; d++) {
             union { s16x4 w[2]; f16x8 v; } f;
 #pragma unroll
             for (int w = 0; w < 2; w++)
-                f.w[w] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lmem4*)((lbyte*)v_part16(lds, d, w) + (AT + u * 16 * DP * 2)));
+                f.w[w] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lmem4*)(uintptr_t)(places.v[d][w] + (AT + u * 16 * DP * 2)));
             v[d] = f.v;
         }
     }
     template <int AT>
-    __device__ __forceinline__ void add16(const char* lds, f32x16 (&x)[NX], const float (&sv)[NX]) {
+    __device__ __forceinline__ void add16(const Places& places, f32x16 (&x)[NX], const float (&sv)[NX]) {
         f16x8 pf[2 * NX], v[2][ND];
         auto step = [&](int u) {
 #pragma unroll
             for (int d = 0; d < ND; d++) o[d] = mfma(v[u % 2][d], pf[u], o[d]);
         };
-        read16<AT>(lds, 0, v[0]);
+        read16<AT>(places, 0, v[0]);
         form(x[0], sv[0], pf);
         __builtin_amdgcn_sched_barrier(0);
-        read16<AT>(lds, 1, v[1]);
+        read16<AT>(places, 1, v[1]);
         step(0);
         if constexpr (NX == 2) {
-            read16<AT>(lds, 2, v[0]);
+            read16<AT>(places, 2, v[0]);
             step(1);
             form(x[1], sv[1], pf + 2);
 #pragma unroll
@@ -454,7 +490,7 @@ struct Rows8 {
                 __builtin_amdgcn_sched_group_barrier(kValu, 80 / (2 * ND), 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            read16<AT>(lds, 3, v[1]);
+            read16<AT>(places, 3, v[1]);
             step(2);
             step(3);
         } else {
@@ -623,6 +659,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
         if (wave < SC / 64) sc[buf * SC + threadIdx.x] = scale;
     };
 
+    const typename R::Places places(lds);
     unsigned long long there = 0, there_next = 0;
     if (s.t0 < s.t1) {
         there = ask_tile(s.t0);
@@ -636,9 +673,9 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
         if (active && j0 <= w.p_hi && (j0 + KT > w.z_lo || j0 < a.sinks)) {
             f32x16 x[R::NX];
             float sv[R::NX];
-            w.template scores16<AT>(lds, x);
+            w.template scores16<AT>(places, x);
             w.scaled(a, sc + buf * SC, j0, there, x, sv);
-            w.template add16<AT + TILE>(lds, x, sv);
+            w.template add16<AT + TILE>(places, x, sv);
         }
         if (t + 1 < s.t1) put_tile(1 - buf);
         __syncthreads();
