@@ -385,7 +385,8 @@ struct Rows8 {
     }
     // The weights of 32 keys.  (l takes them at once: one by one those below half of its
     // last bit would be lost, which a tail of 131071 keys at 2^-25 of the maximum is.)
-    __device__ __forceinline__ void form(f32x16& x, float sv, f16x8* pf) {
+    // `low` (or NULL): what the rounding to fp16 has left of each, as another fp16.
+    __device__ __forceinline__ void form(f32x16& x, float sv, f16x8* pf, f16x8* low = nullptr) {
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; e++) {
@@ -395,6 +396,10 @@ struct Rows8 {
         times_lanes<2>(x, sv);
 #pragma unroll
         for (int e = 0; e < 16; e++) pf[e / 8][e % 8] = (f16)x[e];
+        if (low) {
+#pragma unroll
+            for (int e = 0; e < 16; e++) low[e / 8][e % 8] = (f16)(x[e] - (float)pf[e / 8][e % 8]);
+        }
         l += sum;
     }
     // After the last tile: l with both halves' keys, and m as what a weight of 1 stands
@@ -415,14 +420,9 @@ struct Rows8 {
     // O^T += V^T P^T of the codes at lds + AT, 16 keys a step.  Other tiles are on their
     // way to LDS meanwhile, and the compiler would wait for all of them before the reads'
     // builtin; so two steps of 128 dimensions are read, and waited for, at once.
-    template <int AT>
-    __device__ __forceinline__ void add8(const char* lds, const f16x8 (&pf)[2 * NX]) {
-        static_assert(AT + KT * DP <= 65536, "offsets of a read");
-        two_steps8<AT, 0>(lds, pf);
-        if constexpr (NX == 2) two_steps8<AT, 2>(lds, pf);
-    }
-    template <int AT, int U>
-    __device__ __forceinline__ void two_steps8(const char* lds, const f16x8 (&pf)[2 * NX]) {
+    template <int AT, bool LOW>
+    __device__ __forceinline__ void add8(const char* lds, const f16x8 (&pf)[2 * NX], const f16x8 (&low)[2 * NX]) {
+        static_assert(AT + KT * DP <= 65536 && NX == 1, "offsets of a read");
         constexpr int W = ND < 4 ? 2 : 4;   // runs of 32 dimensions that are read at once
 #pragma unroll
         for (int d = 0; d < ND; d += W) {
@@ -433,7 +433,7 @@ struct Rows8 {
                     "ds_read_b64_tr_b8 %2, %4 offset:%7\n\tds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
                     "s_waitcnt lgkmcnt(0)"
                     : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
-                    : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
+                    : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "n"(AT), "n"(AT + 16 * DP)
                     : "memory");
             else
                 asm volatile(
@@ -445,12 +445,16 @@ struct Rows8 {
                     : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][W - 2]), "=&v"(v[0][W - 1]), "=&v"(v[1][0]), "=&v"(v[1][1]),
                       "=&v"(v[1][W - 2]), "=&v"(v[1][W - 1])
                     : "v"(v_part8(lds, d)), "v"(v_part8(lds, d + 1)), "v"(v_part8(lds, d + 2)), "v"(v_part8(lds, d + 3)),
-                      "n"(AT + U * 16 * DP), "n"(AT + (U + 1) * 16 * DP)
+                      "n"(AT), "n"(AT + 16 * DP)
                     : "memory");
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int c = 0; c < W; c++) o[d + c] = mfma(halves(v[u][c][0], v[u][c][1]), pf[U + u], o[d + c]);
+                for (int c = 0; c < W; c++) {
+                    const f16x8 f = halves(v[u][c][0], v[u][c][1]);
+                    o[d + c] = mfma(f, pf[u], o[d + c]);
+                    if constexpr (LOW) o[d + c] = mfma(f, low[u], o[d + c]);
+                }
         }
     }
     // The weights of a tile and O^T += V^T P^T of the halves at lds + AT.  V's reads run
@@ -739,6 +743,9 @@ template <typename T, typename TO, int DP, int NW>
 __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8Dev a) {
     constexpr int KT = 32, ROWS = 32;
     typedef Rows8<DP, KT> R;
+    // (the matrix cores have time to spare here, so that but for bf16, whose own rounding
+    // is much the larger, weights are taken as two fp16 each)
+    constexpr bool LOW = !std::is_same<TO, bf16>::value;
     constexpr int TILE = KT * DP, SCB = 2 * KT * 4, RING = 4 * TILE + 2 * SCB;   // K, K, V, V, scales, scales
     constexpr int CPR = DP / 16, RPI = 64 / CPR, LOADS = KT / RPI;             // wave loads of a tile
     extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -823,10 +830,9 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
             } else {
                 QGEMV_WAIT("vmcnt(0)");
             }
-            f16x8 pf[2 * R::NX];
-#pragma unroll
-            for (int n = 0; n < R::NX; n++) w.form(x[n], sv[n], pf + 2 * n);
-            w.template add8<(2 + SLOT) * TILE>(mine, pf);
+            f16x8 pf[2], low[2];
+            w.form(x[0], sv[0], pf, LOW ? low : nullptr);
+            w.template add8<(2 + SLOT) * TILE, LOW>(mine, pf, low);
             QGEMV_WAIT("lgkmcnt(0)");
             if (left > 1) load_v(SLOT);
         };
