@@ -352,7 +352,7 @@ struct Rows8 {
         mt = max_halves(mt) * c2;
         bool grows = mt > m + kSlack8;
 #pragma unroll
-        for (int n = 0; n < NX; n++) grows |= sv[n] > r_min;
+        for (int n = 0; n < NX; n++) grows |= fabsf(sv[n]) > r_min;
         if (__any(grows)) {
             // (the largest scale that the row sees here; one that it does not see may be anything)
             const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
@@ -365,7 +365,7 @@ struct Rows8 {
                 // (0 * inf of an unseen scale is NaN, which the maximum passes over)
                 times_lanes<1>(f, sv[n]);
 #pragma unroll
-                for (int e = 0; e < 16; e++) st = fmaxf(st, f[e]);
+                for (int e = 0; e < 16; e++) st = fmaxf(st, fabsf(f[e]));
             }
             st = max_halves(st);
             const int rn = min(max(r, (int)((__builtin_bit_cast(uint32_t, st) + 0x7fffffu) >> 23)), kMost);   // (up to a power of two)

@@ -210,6 +210,32 @@ def test_values_of_zero_and_scales_of_zero(qg):
         within(f64(lse), l, tl)
 
 
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_queries_and_scales_that_are_not_finite_or_negative(qg, kind):
+    """A row of q with NaN or an infinity spoils itself alone; a negative scale is a factor as any other."""
+    g = np.random.default_rng(3)
+    for n in (9, 80):
+        (ck, sk), (cv, sv) = rows8(g, n, 2, 64), rows8(g, n, 2, 64)
+        sk[::3] *= -1
+        sv[:, 1] *= -1
+        pool = [torch.from_numpy(t[None]).to(DEV) for t in (ck, cv, sk, sv)]
+        q = torch.from_numpy(g.standard_normal((n, 4 * 64)).astype(np.float32)).to(TYPES[kind])
+        q[4, 64 + 7], q[6, 3] = float("nan"), float("inf")
+        out = torch.empty(n, 256, device=DEV)
+        start, lens, table = (torch.tensor(t, dtype=torch.int32, device=DEV) for t in ([0, n], [n], [[0]]))
+        say("attn8 odd rows", kind, n)
+        qg.qgemv_paged_attn_q8(qg.kv_cache_q8(*pool), q.to(DEV), TYPE_ID[kind], n, 256, 4, start, lens, 1, n, n, table, 1, 0.125, 0, 0, out, 0, 256)
+        got = f64(out).reshape(n, 4, 64)
+        assert np.isnan(got[4, 1]).all() and np.isnan(got[6, 0]).all()
+        clean = f64(q).reshape(n, 4, 64)
+        clean[~np.isfinite(clean)] = 0
+        o, tol, _, _ = attend8(clean, *(t.astype(np.float64) for t in (ck, sk, cv, np.abs(sv))), np.arange(n), 0, 0, 0.125, "fp32")
+        o[:, 2:] *= -1      # (the second cache head's values are all negative)
+        keep = np.ones((n, 4), bool)
+        keep[4, 1] = keep[6, 0] = False
+        within(got[keep], o[keep], tol[keep])
+
+
 def test_bounds_that_are_larger_than_needed(qg):
     one(qg, [(1, 90), (3, 60)], 4, 2, 64, max_q=50, max_kv=10**9)
     one(qg, [(1, 2900), (3, 60)], 4, 2, 64, max_kv=0)
