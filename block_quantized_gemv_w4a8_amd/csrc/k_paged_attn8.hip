@@ -584,7 +584,16 @@ __device__ __forceinline__ void to_lds16(const void* from, char* to) {
 
 // Many rows: NW waves of 32 rows each, which share every tile of KT keys.  The codes
 // of the next tile are on their way to registers while one is used, and are made fp16
-// once for all waves, on their way to LDS.
+// once for all waves, on their way to LDS (by each wave for itself they would be 160
+// vector instructions a tile, not 20 to 40).  Bound by the vector and the matrix pipe
+// together, which hardly have their work at once: 289 and 32 instructions a wave and
+// tile of 64 keys at 128 dimensions, busy 0.55 and 0.36 of the time at the 1.9 GHz that
+// power leaves.  8192 tokens of 32 heads on 8, causal, take 640 to 650 us, 850 TFLOP/s
+// (with the reads of K one by one and scales read from LDS for every lane 985); nine
+// sequences of chunks of 64 dimensions 58 us.  Four waves at 128 dimensions take as long
+// as eight; three workgroups a CU at 64 dimensions spill, and took 106 us for a prompt of
+// 4096 of 14 heads on 2 where this takes 122, but 50 where this takes 43 for 8 x 512
+// queries over 1500 keys of 16 heads.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     typedef Rows8<DP, KT> R;
@@ -739,6 +748,11 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
 // and scales of two tiles, straight from memory; a tile's K and scales make room for
 // those after next as soon as the scores are formed, and V likewise, so that most
 // of it is always on its way.  Codes become fp16 between LDS and the matrix cores.
+// Bound by the way to memory: 64 sequences of up to 8192 keys, 32 heads on 8 of 128, take
+// 189 us, 4.7 TB/s (the vector pipe is busy 0.4 of the time, the matrix cores 0.13).  Rows
+// of 128 bytes a head, 1 KB apart, are part of that: with the heads' rows of a page
+// together in memory the same takes 175.  Four waves and two workgroups a CU take 200,
+// two or four heads a workgroup 188 to 196, more parts 211.
 template <typename T, typename TO, int DP, int NW>
 __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8Dev a) {
     constexpr int KT = 32, ROWS = 32;
@@ -754,7 +768,8 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     const int half = lane >> 5, row32 = lane & 31;
     // Workgroups go round the eight dies in turn.  A line of scales has a few keys of
     // several heads, so the heads of a part of a sequence run on one die and share it in
-    // its L2.
+    // its L2 (64 sequences of 8192 keys, 32 heads on 8 of 80: 247 -> 182 us, 14 on 2 of 64:
+    // 47 -> 39; with fewer than eight parts dies would be left without work).
     int h = blockIdx.x % a.heads, group = blockIdx.x / a.heads + a.splits * blockIdx.y;
     if (a.by_die) {
         h = blockIdx.x / 8;

@@ -559,9 +559,10 @@ qgemv_status qgemv_rope_append_q8(const qgemv_kv_cache_q8* cache, int64_t T, int
  * numbers, exact in fp16) and q without a rounding that counts (a bf16 row as fp16
  * times a power of two: values below 2^-38 of the row's largest may be lost), a key's scale is
  * multiplied to its score in fp32, and a value's scale to its weight, which is then
- * rounded to fp16 (scaled by powers of two, so that what is lost is below 2^-27
- * of the row's largest weight times its largest seen scale).  Scales of values are
- * meant to be below 2^60, and what scales below 2^-60 contribute may be lost.
+ * rounded to fp16 (scaled by powers of two, so that what is lost is below 2^-31 of the
+ * row's largest weight times its largest seen scale; where a cache head has up to 32
+ * rows and out is not bf16 it is taken as two fp16).  What scales below 2^-60 contribute
+ * may be lost, and rows that see one above 2^60 are slow.
  * Argument conventions, limits and errors as for qgemv_paged_attn. */
 qgemv_status qgemv_paged_attn_q8(const qgemv_kv_cache_q8* cache, const void* q, int q_type,
                                  int64_t T, int64_t ldq, int q_heads, const int32_t* q_start,
