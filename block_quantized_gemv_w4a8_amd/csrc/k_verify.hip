@@ -15,7 +15,8 @@
 //
 // Three launches: the chunks of all rows; for each sequence what is accepted (found
 // again by every workgroup: a few loads) and the sums of what a refused draft leaves of
-// each chunk; the draw.  (With the draw left to the workgroup that comes last, the
+// each chunk; the draw.  Certain drafts leave the chunks' own sums but for one, so the
+// second goes into the third.  (With the draw left to the workgroup that comes last, the
 // releases of memory that this takes made the second launch 31 us of 84.)  48 sequences
 // of up to five rows of 128256 fp32 logits take 48 to 50 us: 29.5, 12.5 and 6.  The first
 // is bound by the vector pipe (0.82 busy, 28 instructions a value of which 17 are the
@@ -418,15 +419,14 @@ __global__ __launch_bounds__(VWG) void k_verify_stats(const VerifyDev a) {
     }
 }
 
-// What is accepted, and the sums of what a refused draft leaves of each chunk, PER a wave.
-template <typename T, int PER>
-__global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
+// What is accepted of a sequence, by a workgroup, for all its threads: the first row
+// whose draft is refused, four rows at a time (the last row has none).
+template <typename T>
+__device__ Choice choose(const VerifyDev& a, int b, const Seq& s) {
     __shared__ int stop;
     __shared__ RowStat at;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.y;
-    const Seq s = sequence(a, b);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const ChunkStat* stats = a.stats + (int64_t)b * a.max_q * a.chunks;
-    // the first row whose draft is refused, four rows at a time: the last row has none
     if (threadIdx.x == 0) {
         stop = s.n > 0 ? s.n - 1 : 0;
         at = RowStat{0.0, -INFINITY, -1};
@@ -449,23 +449,32 @@ __global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
         __syncthreads();
         if (now < i0 + VWAVES) break;
     }
-    const int done = stop;
-    const RowStat r = at;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.choice[b] = Choice{r, done};
-    if (s.n == 0 || s.greedy || done + 1 >= s.n || !a.draft || !(r.inv > 0.0)) return;
+    return Choice{at, stop};
+}
+
+// What is accepted, and the sums of what a refused draft leaves of each chunk, PER a wave.
+template <typename T, int PER>
+__global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.y;
+    const Seq s = sequence(a, b);
+    const Choice pick = choose<T>(a, b, s);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.choice[b] = pick;
+    if (s.n == 0 || s.greedy || pick.done + 1 >= s.n || !(pick.row.inv > 0.0)) return;
     const int c0 = (blockIdx.x * VWAVES + wave) * PER;
     for (int c = c0; c < min(c0 + PER, a.chunks); c++) {
-        const double w = chunk_weight<T>(a, kLeft, s.s0 + done, c, r, s);
+        const double w = chunk_weight<T>(a, kLeft, s.s0 + pick.done, c, pick.row, s);
         if (lane == 0) a.left[(int64_t)b * a.chunks + c] = w;
     }
 }
 
-// The next token.
-template <typename T>
+// The next token; where drafts are certain, what is accepted too.
+template <typename T, bool CERTAIN>
 __global__ __launch_bounds__(VWG) void k_verify_draw(const VerifyDev a) {
     const int b = blockIdx.x;
     const Seq s = sequence(a, b);
-    const Choice pick = a.choice[b];
+    Choice pick;
+    if constexpr (CERTAIN) pick = choose<T>(a, b, s);
+    else pick = a.choice[b];
     const int row = s.s0 + pick.done;
     const bool refused = pick.done + 1 < s.n;
     int next = -1;
@@ -473,7 +482,7 @@ __global__ __launch_bounds__(VWG) void k_verify_draw(const VerifyDev a) {
         next = pick.row.best;
     } else if (s.n > 0 && pick.row.inv > 0.0) {
         const float u = a.u[s.s0];
-        if (refused && a.draft) {
+        if (refused && !CERTAIN) {
             const double* left = a.left + (int64_t)b * a.chunks;
             next = drawn<T>(a, kLeft, row, u, pick.row, s, [&](int c) { return left[c]; });
         }
@@ -563,9 +572,13 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
             const auto one = std::integral_constant<int, 1>{};
             const auto four = std::integral_constant<int, 4>{};
             go(one, false);
+            if (!d.draft) {
+                launch_kernel(k_verify_draw<T, true>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
+                return;
+            }
             if ((int64_t)d.B * d.chunks <= 8192) go(one, true);
             else go(four, true);
-            launch_kernel(k_verify_draw<T>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
+            launch_kernel(k_verify_draw<T, false>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
         } else {
             launch_kernel(k_verify_one<T>, dim3((unsigned)a.B), dim3(VWG),
                           (unsigned)(d.chunks * (sizeof(ChunkStat) + sizeof(double))), st, d);
