@@ -192,10 +192,16 @@ struct Rows8 {
 
     // The rows first_row .. first_row + 31 of the block; this lane's is `row`.  A
     // lane has, of each 32 dimensions, the 16 from `first` on: in two runs of 8
-    // that lie together (JOINED, as a read of 16 codes leaves them) or 16 apart.
+    // that lie together (JOINED, as a read of 16 codes leaves them) or 16 apart.  ask()
+    // sends for q's values, start() takes them: between the two the first tiles are sent for.
+    template <typename T> struct Query {
+        typedef T V8 __attribute__((ext_vector_type(8)));
+        V8 in[NS];
+    };
     template <typename T, bool JOINED>
-    __device__ __forceinline__ void start(const AttnDev& a, const Span& s, int h, int row, int first_row) {
-        const int lane = threadIdx.x & 63, half = lane >> 5;
+    __device__ __forceinline__ Query<T> ask(const AttnDev& a, const Span& s, int h, int row, int first_row) {
+        typedef typename Query<T>::V8 V8;
+        const int half = (threadIdx.x & 63) >> 5;
         const int qi = row / a.G, hq = h * a.G + row - qi * a.G;
         p = s.place(qi);
         z = window_start(a, p);
@@ -203,18 +209,22 @@ struct Rows8 {
         p_hi = s.place(min((first_row + 31) / a.G, s.i1));
         z_lo = window_start(a, s.place(min(first_row / a.G, s.i1)));
         z_hi = window_start(a, p_hi);
-        // (the sign of the scale is moved into q; a scale of 0 is taken in scaled, because
-        // the -inf of a hidden key times 0 would be NaN)
-        c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         const T* q = (const T*)a.q + (int64_t)(s.s0 + qi) * a.ldq + (int64_t)hq * a.D;
-        typedef T V8 __attribute__((ext_vector_type(8)));
-        V8 in[NS];
+        Query<T> r;
 #pragma unroll
         for (int k = 0; k < NS; k++) {
             const int d = JOINED ? 32 * (k / 2) + 16 * half + 8 * (k % 2) : 16 * k + 8 * half;
-            in[k] = V8{};
-            if (d < a.D) in[k] = *reinterpret_cast<const V8*>(q + d);
+            r.in[k] = V8{};
+            if (d < a.D) r.in[k] = *reinterpret_cast<const V8*>(q + d);
         }
+        return r;
+    }
+    template <typename T>
+    __device__ __forceinline__ void start(const AttnDev& a, const Query<T>& query) {
+        const auto& in = query.in;
+        // (the sign of the scale is moved into q; a scale of 0 is taken in scaled, because
+        // the -inf of a hidden key times 0 would be NaN)
+        c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
         float f = a.scale < 0.f ? -1.f : 1.f;
         if constexpr (std::is_same<T, bf16>::value) {
             // bf16 as fp16 times a power of two that takes the row's largest value to 2^14
@@ -625,7 +635,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     const int rc = min(r, r_end - 1);
     const bool active = first_row < r_end;
     R w;
-    w.template start<T, false>(a, s, h, rc, first_row);
+    const auto query = w.template ask<T, false>(a, s, h, rc, first_row);
     pages.arrive(a);
 
     const char* kbase = (const char*)a.k + h * a.head_stride;
@@ -676,7 +686,10 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     unsigned long long there = 0, there_next = 0;
     if (s.t0 < s.t1) {
         there = ask_tile(s.t0);
+        w.start(a, query);
         put_tile(0);
+    } else {
+        w.start(a, query);
     }
     __syncthreads();
     auto step = [&](int t, auto buf) {
@@ -783,7 +796,7 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     if (!make_span<KT, ROWS>(a, b, 0, part, s)) return;
     const int rows = (s.i1 + 1) * a.G;
     R w;
-    w.template start<T, true>(a, s, h, min(row32, rows - 1), 0);
+    const auto query = w.template ask<T, true>(a, s, h, min(row32, rows - 1), 0);
 
     const char* kbase = (const char*)a.k + h * a.head_stride;
     const char* vbase = (const char*)a.v + h * a.head_stride;
@@ -824,6 +837,7 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
             load_k(i);
             load_v(i);
         }
+        w.start(a, query);
         auto step = [&](int t, auto at) {
             constexpr int SLOT = at;
             f32x16 x[R::NX];
@@ -856,6 +870,8 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
             if (t + 1 < t1) step(t + 1, std::integral_constant<int, 1>{});
         }
         w.finish();
+    } else {
+        w.start(a, query);
     }
 
     // the waves' parts of the rows meet in LDS
