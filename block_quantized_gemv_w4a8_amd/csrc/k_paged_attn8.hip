@@ -601,9 +601,8 @@ __device__ __forceinline__ void to_lds16(const void* from, char* to) {
 // power leaves.  8192 tokens of 32 heads on 8, causal, take 640 to 650 us, 850 TFLOP/s
 // (with the reads of K one by one and scales read from LDS for every lane 985); nine
 // sequences of chunks of 64 dimensions 58 us.  Four waves at 128 dimensions take as long
-// as eight; three workgroups a CU at 64 dimensions spill, and took 106 us for a prompt of
-// 4096 of 14 heads on 2 where this takes 122, but 50 where this takes 43 for 8 x 512
-// queries over 1500 keys of 16 heads.
+// as eight.  With the first tile sent for before q is taken, 64 dimensions leave room for
+// three workgroups a CU: a prompt of 4096 of 14 heads on 2 takes 103 us, 122 without.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     typedef Rows8<DP, KT> R;
@@ -762,7 +761,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
 // those after next as soon as the scores are formed, and V likewise, so that most
 // of it is always on its way.  Codes become fp16 between LDS and the matrix cores.
 // Bound by the way to memory: 64 sequences of up to 8192 keys, 32 heads on 8 of 128, take
-// 189 us, 4.7 TB/s (the vector pipe is busy 0.4 of the time, the matrix cores 0.13).  Rows
+// 186 to 189 us, 4.7 TB/s (the vector pipe is busy 0.4 of the time, the matrix cores 0.13).  Rows
 // of 128 bytes a head, 1 KB apart, are part of that: with the heads' rows of a page
 // together in memory the same takes 175.  Four waves and two workgroups a CU take 200,
 // two or four heads a workgroup 188 to 196, more parts 211.
