@@ -601,8 +601,9 @@ __device__ __forceinline__ void to_lds16(const void* from, char* to) {
 // power leaves.  8192 tokens of 32 heads on 8, causal, take 640 to 650 us, 850 TFLOP/s
 // (with the reads of K one by one and scales read from LDS for every lane 985); nine
 // sequences of chunks of 64 dimensions 58 us.  Four waves at 128 dimensions take 715 us
-// where eight take 645: they convert twice as much each.  With the first tile sent for before q is taken, 64 dimensions leave room for
-// three workgroups a CU: a prompt of 4096 of 14 heads on 2 takes 103 us, 122 without.
+// where eight take 645: they convert twice as much each.  With the first tile sent for
+// before q is taken, 64 dimensions leave room for three workgroups a CU: a prompt of 4096
+// of 14 heads on 2 takes 103 us, 122 without.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     typedef Rows8<DP, KT> R;
