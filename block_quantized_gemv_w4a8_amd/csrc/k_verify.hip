@@ -340,7 +340,9 @@ __device__ int drawn(const VerifyDev& a, Kind kind, int row, float u, const RowS
     for (int c = c0; c < c1; c++) {
         const double w = sums(c);
         if (w > 0.0) last = a.chunks - 1 - c;
-        if (found == INT32_MAX && run + w > aim) {
+        // (a thread's first sum may be a last bit above what the thread before it ends with: a
+        // chunk without weight would then pass for the border's)
+        if (found == INT32_MAX && w > 0.0 && run + w > aim) {
             found = c;
             base = run;
         }

@@ -1,0 +1,61 @@
+"""Verification of drafted tokens where sums meet their borders: the token that is drawn has
+a probability above 0."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import block_quantized_gemv_w4a8_amd as qg
+    return qg
+
+
+def call(qg, logits, type_id, start, max_q, tokens, draft, u, ws):
+    T, V = logits.shape
+    B = len(start) - 1
+    start, tokens = (torch.from_numpy(np.asarray(a, np.int32)).to(DEV) for a in (start, tokens))
+    u = torch.from_numpy(np.asarray(u, np.float32)).to(DEV)
+    got = torch.full((2, B), 77, dtype=torch.int32, device=DEV)
+    buf = torch.full((qg.QGEMV_WS_BYTES // 4,), float("nan"), device=DEV) if ws else None
+    qg.qgemv_verify_draft(logits, type_id, T, V, V, start, B, max_q, tokens, draft, V, u, None, got[0], got[1], buf, qg.QGEMV_WS_BYTES if ws else 0)
+    return got.cpu().numpy()
+
+
+WS = [True, False]
+
+
+@pytest.mark.parametrize("ws", WS)
+@pytest.mark.parametrize("drafts", ["none", "certain", "probabilities"])
+def test_chunks_without_mass_are_not_drawn_from(qg, ws, drafts):
+    """Equal logits at 40 tokens, -inf at all others of 52 chunks of 1024: most chunks have no
+    mass, and random numbers that are multiples of 1/8 put every border on a sum of five
+    tokens' weights, 40 u of which lie before it.  Sums of 64 bits may be off by their last
+    one, so the token is the one behind the border or the one before.  With drafts (of a
+    token that has no mass, so that they are refused and all of p is left) alike."""
+    g = np.random.default_rng(1)
+    A, V, rows, eighths = 40, 52 * 1024, 40, 7
+    each = 1 if drafts == "none" else 2
+    allowed = np.sort(np.stack([g.permutation(V - 1)[:A] for _ in range(rows)]), 1)
+    B = rows * eighths
+    logits = torch.full((B, each, V), float("-inf"), dtype=torch.float16, device=DEV)
+    at = torch.from_numpy(np.repeat(allowed, eighths, 0)).to(DEV)
+    logits.scatter_(2, at[:, None].expand(B, each, A), 1.0)
+    u = np.full((B, each), 0.5, np.float32)
+    u[:, 0] = np.tile(np.arange(1, eighths + 1) / 8, rows)
+    draft = None
+    if drafts == "probabilities":
+        draft = torch.zeros(B, each, V, device=DEV)
+        draft[:, 1, V - 1] = 1
+    say("verify empty chunks", ws, drafts)
+    accepted, following = call(qg, logits.view(B * each, V), 1, np.arange(0, B * each + 1, each), each, np.full(B * each, V - 1),
+                               None if draft is None else draft.view(B * each, V), u.reshape(-1), ws)
+    assert not accepted.any()
+    border = (u[:, 0] * A).astype(int)
+    own = np.repeat(allowed, eighths, 0)
+    b = np.arange(B)
+    assert ((following == own[b, border]) | (following == own[b, border - 1])).all()
