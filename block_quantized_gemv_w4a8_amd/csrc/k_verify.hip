@@ -387,7 +387,12 @@ template <typename T>
 __device__ int drawn_whole(const VerifyDev& a, bool refused, int row, float u, const RowStat& r, const Seq& s, const ChunkStat* stats) {
     __shared__ double rest;
     if (!(r.inv > 0.0)) return -1;
-    const auto whole = [&](int c) { return chunk_mass(stats[c], r.top, s) * r.inv; };
+    // (by p of the chunk's largest: where that is 0 its tokens weigh nothing one by one either,
+    // while a sum of their exponentials may still hold a bit)
+    const auto whole = [&](int c) {
+        const ChunkStat k = stats[c];
+        return k.sum > 0.0 ? k.sum * prob(k.top, r, s) : 0.0;
+    };
     if (refused && !a.draft) {
         const int token = a.tokens[row + 1], its = token >= 0 && token < a.V ? token / VCH : -1;
         if (threadIdx.x < 64 && its >= 0) {

@@ -59,3 +59,25 @@ def test_chunks_without_mass_are_not_drawn_from(qg, ws, drafts):
     own = np.repeat(allowed, eighths, 0)
     b = np.arange(B)
     assert ((following == own[b, border]) | (following == own[b, border - 1])).all()
+
+
+@pytest.mark.parametrize("ws", WS)
+@pytest.mark.parametrize("drafts", ["none", "certain"])
+def test_a_chunk_whose_tokens_weigh_nothing_is_not_drawn_from(qg, ws, drafts):
+    """700 tokens at 0 in the last chunk, and in the first, behind 100 that are -inf, 924 at
+    -744.4: exp is 2^-1074 there, the least number of 64 bits, so p = exp / 700 is 0 for each of
+    them while their sum over 700 is not.  A random number of 0 takes the first token with a
+    probability, and one of 1 the last."""
+    V, B = 3 * 1024, 4
+    each = 1 if drafts == "none" else 2
+    for flip in (False, True):
+        row = torch.full((V,), float("-inf"))
+        row[100:1024], row[2048 + 200:2048 + 900] = -744.4, 0.0
+        row = row.flip(0) if flip else row
+        logits = row.repeat(B * each, 1).to(DEV)
+        u = np.full((B, each), 0.5, np.float32)
+        u[:, 0] = 1.0 if flip else 0.0
+        say("verify weightless chunk", ws, drafts, flip)
+        accepted, following = call(qg, logits, 0, np.arange(0, B * each + 1, each), each, np.full(B * each, 1500), None, u.reshape(-1), ws)
+        mass = np.nonzero((row == 0).numpy())[0]
+        assert not accepted.any() and (following == mass[-1 if flip else 0]).all(), (following, mass[[0, -1]])
