@@ -7,8 +7,8 @@
 // the keys with the running maximum and sum of a softmax.  Codes are whole numbers
 // that fp16 holds, so they go to the fp16 matrix cores exactly and the scales are
 // taken in fp32 on both sides of them: a key's multiplies its score, a value's its
-// weight.  The weight is then rounded to fp16, with factors of two that keep it in
-// fp16's range (kLift, and the largest scale that the row has seen).
+// weight.  The weight is then rounded to fp16, or to two that add up to it, with factors
+// of two that keep it in fp16's range (kLift, and the largest scale that the row has seen).
 //
 // Rows, tiles and their order are those of the attention over 16-bit values: the
 // queries of a sequence times the G query heads of a cache head, 32 rows a wave, X^T
@@ -467,9 +467,9 @@ struct Rows8 {
                 }
         }
     }
-    // The weights of a tile and O^T += V^T P^T of the halves at lds + AT.  V's reads run
-    // ahead, and the weights of the second 32 keys are formed beside the products of the
-    // first.
+    // The weights of a tile (LOW: as two fp16 each) and O^T += V^T P^T of the halves at lds
+    // + AT.  V's reads run ahead, and the weights of the second 32 keys are formed beside the
+    // products of the first.
     template <int AT>
     __device__ __forceinline__ void read16(const Places& places, int u, f16x8 (&v)[ND]) {
 #pragma unroll
@@ -481,27 +481,30 @@ struct Rows8 {
             v[d] = f.v;
         }
     }
-    template <int AT>
+    template <int AT, bool LOW>
     __device__ __forceinline__ void add16(const Places& places, f32x16 (&x)[NX], const float (&sv)[NX]) {
-        f16x8 pf[2 * NX], v[2][ND];
+        f16x8 pf[2 * NX], low[2 * NX], v[2][ND];
         auto step = [&](int u) {
 #pragma unroll
-            for (int d = 0; d < ND; d++) o[d] = mfma(v[u % 2][d], pf[u], o[d]);
+            for (int d = 0; d < ND; d++) {
+                o[d] = mfma(v[u % 2][d], pf[u], o[d]);
+                if constexpr (LOW) o[d] = mfma(v[u % 2][d], low[u], o[d]);
+            }
         };
         read16<AT>(places, 0, v[0]);
-        form(x[0], sv[0], pf);
+        form(x[0], sv[0], pf, LOW ? low : nullptr);
         __builtin_amdgcn_sched_barrier(0);
         read16<AT>(places, 1, v[1]);
         step(0);
         if constexpr (NX == 2) {
             read16<AT>(places, 2, v[0]);
             step(1);
-            form(x[1], sv[1], pf + 2);
+            form(x[1], sv[1], pf + 2, LOW ? low + 2 : nullptr);
 #pragma unroll
             for (int i = 0; i < 2 * ND; i++) {
                 __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
-                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(kValu, 80 / (2 * ND), 0);
+                __builtin_amdgcn_sched_group_barrier(kMfma, LOW ? 2 : 1, 0);
+                __builtin_amdgcn_sched_group_barrier(kValu, (LOW ? 112 : 80) / (2 * ND), 0);
             }
             __builtin_amdgcn_sched_barrier(0);
             read16<AT>(places, 3, v[1]);
@@ -611,6 +614,11 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     constexpr int TILE = KT * DP * 2, BUF = 2 * TILE;    // bytes of a K (or V) tile, and of both
     constexpr int LOADS = KT / RPI / NW;                 // wave loads of K (and of V) per wave
     constexpr int SC = 2 * KT;                           // scales of a tile
+    // (one fp16 a weight, off by up to 2^-11, would be the whole error of an fp32 output: it takes
+    // two, 2^-22.  Of fp16 outputs one leaves 2.9e-4 where their own rounding leaves 2.1e-4.  A
+    // prompt of 8192, 32 heads on 8 of 128, takes 890 us so, 670 to 680 with one; 4096 tokens of
+    // 14 on 2 of 64 136 and 96, of 8 on 2 of 256 261 and 230)
+    constexpr bool LOW = std::is_same<TO, float>::value;
     static_assert(LOADS >= 1 && KT <= 64 && SC <= 64 * NW && SC % 64 == 0, "tile shape");
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     float* sc = reinterpret_cast<float*>(lds + 2 * BUF);
@@ -701,7 +709,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
             float sv[R::NX];
             w.template scores16<AT>(places, x);
             w.scaled(a, sc + buf * SC, j0, there, x, sv);
-            w.template add16<AT + TILE>(places, x, sv);
+            w.template add16<AT + TILE, LOW>(places, x, sv);
         }
         if (t + 1 < s.t1) put_tile(1 - buf);
         __syncthreads();

@@ -560,9 +560,10 @@ qgemv_status qgemv_rope_append_q8(const qgemv_kv_cache_q8* cache, int64_t T, int
  * times a power of two: values below 2^-38 of the row's largest may be lost), a key's scale is
  * multiplied to its score in fp32, and a value's scale to its weight, which is then
  * rounded to fp16 (scaled by powers of two, so that what is lost is below 2^-31 of the
- * row's largest weight times its largest seen scale; where a cache head has up to 32
- * rows and out is not bf16 it is taken as two fp16).  What scales below 2^-60 contribute
- * may be lost, and rows that see one above 2^60 are slow.
+ * row's largest weight times its largest seen scale).  It is taken as two fp16, which
+ * leaves 2^-22 of it, where out is fp32, and for fp16 where max_q times the heads of a
+ * group is at most 32.  What scales below 2^-60 contribute may be lost, and rows that see
+ * one above 2^60 are slow.
  * Argument conventions, limits and errors as for qgemv_paged_attn. */
 qgemv_status qgemv_paged_attn_q8(const qgemv_kv_cache_q8* cache, const void* q, int q_type,
                                  int64_t T, int64_t ldq, int q_heads, const int32_t* q_start,
