@@ -23,7 +23,6 @@
 // exponential and its sum; the bytes take 3.8 TB/s), the others by the way through stats,
 // logits and sums.
 #include <algorithm>
-#include <type_traits>
 
 #include "qgemv_layer.h"
 
@@ -133,7 +132,7 @@ __device__ __forceinline__ float logit(const T* row, int v) {
     return real((float)row[v]);
 }
 
-// Sixteen values of chunk c of a row, `none` past its end; value i of lane l is
+// Sixteen values of chunk c of a row, -inf past its end; value i of lane l is
 // number place<T>(c, i) of the row.  (Rows need no alignment beyond their elements'.)
 template <typename T>
 __device__ __forceinline__ int place(int c, int i) {
@@ -141,7 +140,7 @@ __device__ __forceinline__ int place(int c, int i) {
     return c * VCH + i / G * (64 * G) + (threadIdx.x & 63) * G + i % G;
 }
 template <typename T>
-__device__ __forceinline__ void chunk_values(const T* row, int V, int c, float none, float (&x)[VPL]) {
+__device__ __forceinline__ void chunk_values(const T* row, int V, int c, float (&x)[VPL]) {
     constexpr int G = 16 / sizeof(T);
 #pragma unroll
     for (int i = 0; i < VPL; i += G) {
@@ -153,7 +152,7 @@ __device__ __forceinline__ void chunk_values(const T* row, int V, int c, float n
             for (int j = 0; j < G; j++) x[i + j] = (float)e[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < G; j++) x[i + j] = v + j < V ? (float)row[v + j] : none;
+            for (int j = 0; j < G; j++) x[i + j] = v + j < V ? (float)row[v + j] : -INFINITY;
         }
     }
 }
@@ -271,12 +270,12 @@ __device__ __forceinline__ double weight(const VerifyDev& a, Kind kind, int row,
     const double w = p - (q > 0.f ? (double)q : 0.0);
     return w > 0.0 ? w : 0.0;
 }
-// The sum over a chunk, by a wave, of a row that has mass.
+// The sum of what a draft leaves of a chunk, by a wave, of a row that has mass.
 template <typename T>
-__device__ double chunk_weight(const VerifyDev& a, Kind kind, int row, int c, const RowStat& r, const Seq& s) {
+__device__ double chunk_left(const VerifyDev& a, int row, int c, const RowStat& r, const Seq& s) {
     float x[VPL], q[VPL] = {};
-    chunk_values((const T*)a.logits + (int64_t)row * a.ldl, a.V, c, -INFINITY, x);
-    if (kind == kLeft && a.draft) {
+    chunk_values((const T*)a.logits + (int64_t)row * a.ldl, a.V, c, x);
+    if (a.draft) {
         // (at the places of x)
         constexpr int G = 16 / sizeof(T);
         const float* d = a.draft + (int64_t)(row + 1) * a.ldd;
@@ -290,7 +289,7 @@ __device__ double chunk_weight(const VerifyDev& a, Kind kind, int row, int c, co
     }
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; i++) sum += weight(a, kind, row, place<T>(c, i), x[i], q[i], r, s);
+    for (int i = 0; i < VPL; i++) sum += weight(a, kLeft, row, place<T>(c, i), x[i], q[i], r, s);
     return wave_sum(sum);
 }
 
@@ -396,7 +395,7 @@ __device__ int drawn_whole(const VerifyDev& a, bool refused, int row, float u, c
     if (refused && !a.draft) {
         const int token = a.tokens[row + 1], its = token >= 0 && token < a.V ? token / VCH : -1;
         if (threadIdx.x < 64 && its >= 0) {
-            const double w = chunk_weight<T>(a, kLeft, row, its, r, s);
+            const double w = chunk_left<T>(a, row, its, r, s);
             if (threadIdx.x == 0) rest = w;
         }
         __syncthreads();
@@ -406,24 +405,16 @@ __device__ int drawn_whole(const VerifyDev& a, bool refused, int row, float u, c
     return drawn<T>(a, kWhole, row, u, r, s, whole);
 }
 
-// The chunks of all rows, PER a wave, the next on its way while one is summed.
-template <typename T, int PER>
+// The chunks of all rows, one a wave.
+template <typename T>
 __global__ __launch_bounds__(VWG) void k_verify_stats(const VerifyDev a) {
-    const int c0 = (blockIdx.x * VWAVES + (threadIdx.x >> 6)) * PER, i = blockIdx.y, b = blockIdx.z;
+    const int c = blockIdx.x * VWAVES + (threadIdx.x >> 6), i = blockIdx.y, b = blockIdx.z;
     const Seq s = sequence(a, b);
-    if (i >= s.n || c0 >= a.chunks) return;
-    const T* row = (const T*)a.logits + (int64_t)(s.s0 + i) * a.ldl;
-    ChunkStat* to = a.stats + ((int64_t)b * a.max_q + i) * a.chunks;
-    float x[2][VPL];
-    chunk_values(row, a.V, c0, -INFINITY, x[0]);
-#pragma unroll
-    for (int k = 0; k < PER; k++) {
-        const int c = c0 + k;
-        if (c >= a.chunks) break;
-        if (k + 1 < PER && c + 1 < a.chunks) chunk_values(row, a.V, c + 1, -INFINITY, x[(k + 1) % 2]);
-        const ChunkStat r = chunk_stat<T>(x[k % 2], c, s);
-        if ((threadIdx.x & 63) == 0) to[c] = r;
-    }
+    if (i >= s.n || c >= a.chunks) return;
+    float x[VPL];
+    chunk_values((const T*)a.logits + (int64_t)(s.s0 + i) * a.ldl, a.V, c, x);
+    const ChunkStat r = chunk_stat<T>(x, c, s);
+    if ((threadIdx.x & 63) == 0) a.stats[((int64_t)b * a.max_q + i) * a.chunks + c] = r;
 }
 
 // What is accepted of a sequence, by a workgroup, for all its threads: the first row
@@ -469,7 +460,7 @@ __global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
     if (s.n == 0 || s.greedy || pick.done + 1 >= s.n || !(pick.row.inv > 0.0)) return;
     const int c0 = (blockIdx.x * VWAVES + wave) * PER;
     for (int c = c0; c < min(c0 + PER, a.chunks); c++) {
-        const double w = chunk_weight<T>(a, kLeft, s.s0 + pick.done, c, pick.row, s);
+        const double w = chunk_left<T>(a, s.s0 + pick.done, c, pick.row, s);
         if (lane == 0) a.left[(int64_t)b * a.chunks + c] = w;
     }
 }
@@ -516,7 +507,7 @@ __global__ __launch_bounds__(VWG) void k_verify_one(const VerifyDev a) {
         __syncthreads();
         for (int c = wave; c < a.chunks; c += VWAVES) {
             float x[VPL];
-            chunk_values((const T*)a.logits + (int64_t)row * a.ldl, a.V, c, -INFINITY, x);
+            chunk_values((const T*)a.logits + (int64_t)row * a.ldl, a.V, c, x);
             const ChunkStat st = chunk_stat<T>(x, c, s);
             if (lane == 0) stats[c] = st;
         }
@@ -534,7 +525,7 @@ __global__ __launch_bounds__(VWG) void k_verify_one(const VerifyDev a) {
         const float u = a.u[s.s0];
         if (refused && a.draft && r.inv > 0.0) {
             for (int c = wave; c < a.chunks; c += VWAVES) {
-                const double w = chunk_weight<T>(a, kLeft, row, c, r, s);
+                const double w = chunk_left<T>(a, row, c, r, s);
                 if (lane == 0) sums[c] = w;
             }
             __syncthreads();
@@ -570,21 +561,14 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
         // (few chunks of few sequences: one workgroup each.  4 rows of 2000 values take 11.7 us, by
         // three launches 14.3; of 10000 values 19.4 and 14.5; 8 sequences of 4 rows of 600 15.9 and 15.5)
         if (fits && ((int64_t)d.chunks * d.max_q > 16 || d.B > 4)) {
-            const auto go = [&](auto per, bool last) {
-                constexpr int PER = decltype(per)::value;
-                const unsigned x = (unsigned)((d.chunks + VWAVES * PER - 1) / (VWAVES * PER));
-                if (last) launch_kernel(k_verify_left<T, PER>, dim3(x, (unsigned)d.B), dim3(VWG), 0, st, d);
-                else launch_kernel(k_verify_stats<T, PER>, dim3(x, (unsigned)d.max_q, (unsigned)d.B), dim3(VWG), 0, st, d);
-            };
-            const auto one = std::integral_constant<int, 1>{};
-            const auto four = std::integral_constant<int, 4>{};
-            go(one, false);
+            const auto groups = [&](int per) { return (unsigned)((d.chunks + VWAVES * per - 1) / (VWAVES * per)); };
+            launch_kernel(k_verify_stats<T>, dim3(groups(1), (unsigned)d.max_q, (unsigned)d.B), dim3(VWG), 0, st, d);
             if (!d.draft) {
                 launch_kernel(k_verify_draw<T, true>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
                 return;
             }
-            if ((int64_t)d.B * d.chunks <= 8192) go(one, true);
-            else go(four, true);
+            if ((int64_t)d.B * d.chunks <= 8192) launch_kernel(k_verify_left<T, 1>, dim3(groups(1), (unsigned)d.B), dim3(VWG), 0, st, d);
+            else launch_kernel(k_verify_left<T, 4>, dim3(groups(4), (unsigned)d.B), dim3(VWG), 0, st, d);
             launch_kernel(k_verify_draw<T, false>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
         } else {
             launch_kernel(k_verify_one<T>, dim3((unsigned)a.B), dim3(VWG),
