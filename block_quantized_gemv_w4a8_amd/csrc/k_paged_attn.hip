@@ -455,7 +455,7 @@ __global__ __launch_bounds__(64 * NW, OCC) void k_attn_many(const AttnDev a) {
     const int64_t tok = s.s0 + qi, row = tok * a.q_heads + hq;
     if (own && !bad) {
         const int64_t at = row * a.splits + part;
-        const float inv = s.parts > 1 ? 1.f : row_scale(w.l);
+        const float inv = s.parts > 1 ? 1.f : row_inverse(w.l);
         TO* out = (TO*)a.out + tok * a.ldo + (int64_t)hq * a.D;
 #pragma unroll
         for (int d = 0; d < R::ND; d++)

@@ -86,7 +86,7 @@ __device__ __forceinline__ int64_t key_offset(const AttnDev& a, int page, int j)
 }
 
 // m is in units of log2; 1 / l of a row that saw nothing is 0.
-__device__ __forceinline__ float row_scale(float l) { return l != 0.f ? 1.f / l : 0.f; }
+__device__ __forceinline__ float row_inverse(float l) { return l != 0.f ? 1.f / l : 0.f; }
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -107,7 +107,7 @@ __device__ void put_row(const AttnDev& a, const Span& s, int part, int i, int hq
         }
         return;
     }
-    const float inv = row_scale(l);
+    const float inv = row_inverse(l);
     TO* out = (TO*)a.out + t * a.ldo + (int64_t)hq * a.D;
     for (int c = 0; c < 4; c++)
         if (lane + 64 * c < a.D) out[lane + 64 * c] = (TO)(o[c] * inv);
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnDev a) {
 #pragma unroll 4
     for (int w = AHEAD; w < s.parts; w++)
         join(ml[2 * w], ml[2 * w + 1], *reinterpret_cast<const f32x4v*>(po + (int64_t)w * a.D));
-    const float inv = row_scale(sum);
+    const float inv = row_inverse(sum);
 #pragma unroll
     for (int c = 0; c < 4; c++) f[c] *= inv;
     store4((TO*)a.out + tok * a.ldo + (int64_t)hq * a.D + d, f);
