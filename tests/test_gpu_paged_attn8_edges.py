@@ -1,4 +1,5 @@
-"""Attention over the 8-bit paged cache: what an output in 32 bits holds."""
+"""Attention over the 8-bit paged cache: what an output in 32 bits holds, and pools of more than
+2^32 bytes whose pages are whole runs."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +79,32 @@ def test_an_output_in_32_bits_has_more_than_16(qg, kind, D, counts):
         o, tol = close(f64(q).reshape(T, Hq, D)[r], *rows[b], np.arange(L - n, L), D**-0.5)
         within(got[r], o, tol, f"sequence {b}")
     assert pool
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_whole_pages_past_32_bits(qg, D):
+    """Pages less than 2^31 bytes apart, whose places are formed from 32-bit strides: the last ones
+    begin past 2^32 bytes of codes and past 2^32 elements of scales."""
+    far, pages, page = 2**30 + 2**20, 6, 16
+    codes = torch.empty((pages - 1) * far + 2 * page * D, dtype=torch.int8, device=DEV)
+    k, v = (codes[i * page * D:].as_strided((pages, page, 1, D), (far, D, D, 1)) for i in range(2))
+    scales = torch.empty((pages - 1) * far + 2 * page, device=DEV)
+    ks, vs = (scales[i * page:].as_strided((pages, page, 1), (far, 1, 1)) for i in range(2))
+    g = np.random.default_rng(D)
+    L, order = pages * page, [5, 0, 4, 2, 1, 3]
+    rows = []
+    for _ in range(2):
+        rows.append(np.clip(np.rint(g.standard_normal((L, 1, D)) * 42), -127, 127).astype(np.int8))
+        rows.append((0.01 * 4.0 ** g.random((L, 1))).astype(np.float32))
+    for i, at in enumerate(order):
+        for t, r in zip((k, ks, v, vs), rows):
+            t[at] = torch.from_numpy(r[page * i:page * i + page]).to(DEV)
+    table = torch.tensor([order], dtype=torch.int32, device=DEV)
+    cache = qg.kv_cache_q8(k, v, ks, vs)
+    for n in (1, 90):
+        say("attn8 whole pages past 32 bits", D, n)
+        q, out = torch.randn(n, D, device=DEV).bfloat16(), torch.zeros(n, D, device=DEV).bfloat16()
+        start, lens = (torch.tensor(t, dtype=torch.int32, device=DEV) for t in ([0, n], [L]))
+        qg.qgemv_paged_attn_q8(cache, q, 2, n, D, 1, start, lens, 1, n, L, table, pages, 0.125, 0, 0, out, 2, D)
+        o, tol, _, _ = attend8(f64(q)[:, None], *(r.astype(np.float64) for r in rows), np.arange(L - n, L), 0, 0, 0.125, "bf16")
+        within(f64(out)[:, None], o, tol)

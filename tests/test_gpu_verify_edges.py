@@ -1,10 +1,11 @@
-"""Verification of drafted tokens where sums meet their borders: the token that is drawn has
-a probability above 0."""
+"""Verification of drafted tokens where sums meet their borders (the token that is drawn has a
+probability above 0), and at its largest size."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import DEV, say
+from test_gpu_verify import one
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +82,11 @@ def test_a_chunk_whose_tokens_weigh_nothing_is_not_drawn_from(qg, ws, drafts):
         accepted, following = call(qg, logits, 0, np.arange(0, B * each + 1, each), each, np.full(B * each, 1500), None, u.reshape(-1), ws)
         mass = np.nonzero((row == 0).numpy())[0]
         assert not accepted.any() and (following == mass[-1 if flip else 0]).all(), (following, mass[[0, -1]])
+
+
+@pytest.mark.parametrize("ws", WS)
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_a_row_of_the_largest_vocabulary(qg, ws, kind):
+    """2^22 values a row, 4096 chunks: one workgroup's work takes 98304 bytes of LDS for them."""
+    one(qg, [2, 1], 1 << 22, kind, ws=ws, near=0.1)
+    one(qg, [2], 1 << 22, kind, ws=ws, draft=False)
