@@ -789,8 +789,7 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     const int half = lane >> 5, row32 = lane & 31;
     // Workgroups go round the eight dies in turn.  A line of scales has a few keys of
     // several heads, so the heads of a part of a sequence run on one die and share it in
-    // its L2 (64 sequences of 8192 keys, 32 heads on 8 of 80: 247 -> 182 us, 14 on 2 of 64:
-    // 47 -> 39; with fewer than eight parts dies would be left without work).
+    // its L2 (the rule is at the launch).
     int h = blockIdx.x % a.heads, group = blockIdx.x / a.heads + a.splits * blockIdx.y;
     if (a.by_die) {
         h = blockIdx.x / 8;
@@ -934,8 +933,16 @@ static void launch_many(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
 template <typename T, typename TO, int DP, int NW>
 static void launch_few(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
     split(d, a.max_kv, 32, 32, 4 * NW, 256, 0, a.ws_bytes, a.ws);
-    const int64_t groups = (int64_t)d.B * d.splits;
-    d.by_die = groups >= 8;
+    // The heads of a part on one die, or each where its turn comes.  64 sequences of 8192 keys, 32
+    // heads on 8 of 80: 182 and 247 us, of 128 187 and 198, 14 on 2 of 64 38 and 47.  A die then has
+    // up to `heads` workgroups more than another, and 32 CUs (two workgroups each at 64 dimensions):
+    // with up to 16 cache heads, over 66 sizes of 9 to 100 parts of up to 3000 keys, one die took
+    // 0.74 to 1.05 of the time, 0.94 in the mean.  With 20 to 64 it took up to 1.6 where some dies
+    // have a part more (9 parts of 32 on 32 of 128: 67 and 42 us; 33: 166 and 143), and 0.84 to 1.06
+    // where they have a ninth more at the most (65 and 100 parts).  With fewer than eight parts
+    // dies would be left without work (6 of 4096 keys, 32 on 32 of 128: 56 and 55 us).
+    const int64_t groups = (int64_t)d.B * d.splits, dealt = (groups + 7) / 8 * 8;
+    d.by_die = groups >= 8 && (d.heads <= 16 || 9 * dealt < 10 * groups);
     launch_kernel(k_attn8_few<T, TO, DP, NW>,
                   d.by_die ? dim3(8u * d.heads, (unsigned)((groups + 7) / 8)) : dim3((unsigned)(d.heads * d.splits), (unsigned)d.B),
                   dim3(64 * NW), NW * (4 * 32 * DP + 512 + 256), st, d);

@@ -7,6 +7,7 @@ import torch
 from cache8_ref import LOST, attend8
 from gpu_util import DEV, say
 from layer_ref import F32, TYPE_ID, TYPES, f64, rounded, within
+from test_gpu_paged_attn8 import one
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +109,12 @@ def test_whole_pages_past_32_bits(qg, D):
         qg.qgemv_paged_attn_q8(cache, q, 2, n, D, 1, start, lens, 1, n, L, table, pages, 0.125, 0, 0, out, 2, D)
         o, tol, _, _ = attend8(f64(q)[:, None], *(r.astype(np.float64) for r in rows), np.arange(L - n, L), 0, 0, 0.125, "bf16")
         within(f64(out)[:, None], o, tol)
+
+
+@pytest.mark.parametrize("H,D", [(1, 64), (16, 64), (20, 64), (20, 128)])
+@pytest.mark.parametrize("parts", [7, 8, 9, 12, 16])
+def test_cache_heads_and_parts_on_both_sides_of_the_dealing(qg, H, D, parts):
+    """Single tokens of so many sequences, by which it is chosen where a part's heads run: one result
+    for each head of each."""
+    one(qg, [(1, 5 + 3 * b) for b in range(parts)], H, H, D, page=16, out_kind="fp32")
+    one(qg, [(1, 40 + b) for b in range(parts)], 2 * H, H, D, page=16, ws=False)
