@@ -44,7 +44,8 @@ __device__ __forceinline__ float turned(float x, float c, float y, float s) {
 // LPR lanes a row (a power of two, at least D / 8).  Bound by memory and by the way
 // to the angles, which stand before a workgroup's work: 8192 tokens of 48 heads of 128,
 // half of each rotated, 48.6 us, 3.8 TB/s of 5.3 that a copy reaches (with a row's loads
-// ahead of the row before it 54).
+// ahead of the row before it 54); all of each 53, by pairs 41.  kSingle reads partners one by
+// one: 122 of 128 values rotated 71 us, by pairs 83.
 template <typename TI, typename TQ, RopeWalk WALK, int LPR>
 __global__ __launch_bounds__(RWG) void k_rope_append8(const Rope8Dev a) {
     __shared__ float2 cs[QGEMV_HEAD_DIM_MAX / 2];
@@ -145,7 +146,8 @@ hipError_t launch_rope_append_q8(const Rope8Args& a, hipStream_t st) {
             using TQ = decltype(tq);
             auto go = [&](auto kernel, int lpr) {
                 // few tokens: all of a token's rows at once; many: one workgroup a token,
-                // which forms its angles once
+                // which forms its angles once (48 heads of 128 in three parts: 1 token 3.5 us and
+                // 4.8, 256 5.3 and 6.4, 512 6.9 and 7.4, 768 9.3 and 9.1, 2048 17.2 and 16.2, 8192 65 and 52)
                 const int64_t rows = (int64_t)d.q_heads + 2 * d.heads;
                 const int64_t parts = (rows * lpr + RWG - 1) / RWG;
                 for (d.first = 0; d.first < a.T; d.first += kTokens)

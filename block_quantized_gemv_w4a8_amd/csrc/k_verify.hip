@@ -558,8 +558,11 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
     d.stats = (ChunkStat*)((char*)a.ws + choice + left);
     with_type(a.logits_type, [&](auto t) {
         using T = decltype(t);
-        // (few chunks of few sequences: one workgroup each.  4 rows of 2000 values take 11.7 us, by
-        // three launches 14.3; of 10000 values 19.4 and 14.5; 8 sequences of 4 rows of 600 15.9 and 15.5)
+        // (few chunks of few sequences: one workgroup each.  With probabilities, against three launches:
+        // 4 rows of 2000 values 11.3 us and 13.1, of 4096 11.9 and 13.0, of 6000 20.7 and 11.9; 4 sequences
+        // of 2 rows of 4096 10.1 and 12.7, of 4 14.2 and 13.7, 8 of 4 15.4 and 15.0.  Certain drafts,
+        // against two: 1 row of 600 7.4 and 9.2, 4 of 2000 10.0 and 11.5, of 4096 9.9 and 11.4, of 6000 20.7
+        // and 10.2; 4 sequences of 2 rows of 4096 10.1 and 11.6, of 4 12.0 and 11.8, 8 of 4 12.9 and 11.9)
         if (fits && ((int64_t)d.chunks * d.max_q > 16 || d.B > 4)) {
             const auto groups = [&](int per) { return (unsigned)((d.chunks + VWAVES * per - 1) / (VWAVES * per)); };
             launch_kernel(k_verify_stats<T>, dim3(groups(1), (unsigned)d.max_q, (unsigned)d.B), dim3(VWG), 0, st, d);
@@ -567,7 +570,9 @@ hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t st) {
                 launch_kernel(k_verify_draw<T, true>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
                 return;
             }
-            if ((int64_t)d.B * d.chunks <= 8192) launch_kernel(k_verify_left<T, 1>, dim3(groups(1), (unsigned)d.B), dim3(VWG), 0, st, d);
+            // (chunks a wave: 9072 in all, 72 sequences of 126, take 39 us by one and 41 by four, 12800 47
+            // and 48, 16128 53 and 51; 32000 100 and 95)
+            if ((int64_t)d.B * d.chunks <= 15 << 10) launch_kernel(k_verify_left<T, 1>, dim3(groups(1), (unsigned)d.B), dim3(VWG), 0, st, d);
             else launch_kernel(k_verify_left<T, 4>, dim3(groups(4), (unsigned)d.B), dim3(VWG), 0, st, d);
             launch_kernel(k_verify_draw<T, false>, dim3((unsigned)d.B), dim3(VWG), 0, st, d);
         } else {

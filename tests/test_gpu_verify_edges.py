@@ -90,3 +90,9 @@ def test_a_row_of_the_largest_vocabulary(qg, ws, kind):
     """2^22 values a row, 4096 chunks: one workgroup's work takes 98304 bytes of LDS for them."""
     one(qg, [2, 1], 1 << 22, kind, ws=ws, near=0.1)
     one(qg, [2], 1 << 22, kind, ws=ws, draft=False)
+
+
+def test_so_many_chunks_that_a_wave_takes_four(qg):
+    """970 sequences of 16 chunks, the last of 640 values, with what drafts leave of each."""
+    accepted, _ = one(qg, [2] * 970, 16000)
+    assert set(accepted) == {0, 1}
