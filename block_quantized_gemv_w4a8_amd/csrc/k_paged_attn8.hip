@@ -602,11 +602,14 @@ __device__ __forceinline__ void to_lds16(const void* from, char* to) {
 // together, which hardly have their work at once: 289 and 32 instructions a wave and
 // tile of 64 keys at 128 dimensions, busy 0.55 and 0.36 of the time at the 1.9 GHz that
 // power leaves.  8192 tokens of 32 heads on 8, causal, take 640 to 650 us, 850 TFLOP/s
-// (with the reads of K one by one and scales read from LDS for every lane 985); nine
-// sequences of chunks of 64 dimensions 58 us.  Four waves at 128 dimensions take 715 us
+// (with the reads of K one by one and scales read from LDS for every lane 985).  Nine
+// sequences of chunks of 64 dimensions take 58 us: 0.36 of a wave's time it waits for the tile
+// that the step before sent for, vector pipe 0.48 busy.  Four waves at 128 dimensions take 715 us
 // where eight take 645: they convert twice as much each.  With the first tile sent for
 // before q is taken, 64 dimensions leave room for three workgroups a CU: a prompt of 4096
 // of 14 heads on 2 takes 103 us, 122 without.
+// 256 dimensions: one wave a SIMD, and a prompt of 4096 of 8 heads on 2 is one round of 256
+// workgroups whose longest, 128 tiles of 1.8 us, is its 230 us.
 template <typename T, typename TO, int DP, int KT, int NW, int OCC>
 __global__ __launch_bounds__(64 * NW, OCC) void k_attn8_many(const Attn8Dev a) {
     typedef Rows8<DP, KT> R;
@@ -921,6 +924,11 @@ __global__ __launch_bounds__(64 * NW, (NW + 3) / 4) void k_attn8_few(const Attn8
     }
 }
 
+// (The rule and its places are those of the attention over 16 bits, though a CU holds three
+// workgroups of 64 dimensions here, two with an fp32 output.  Over 14 sizes of 300 to 4096
+// queries 768 places for 512 and for 1024 took 0.96 of the time, 0.81 to 1.12 (2 x 2000 queries over
+// 4000 keys, 14 heads on 2, 125 us and 102; 4 x 300 over 8192, 16 on 16, 81 and 90), and with fp32
+// out 1.00, 0.78 to 1.27.)
 template <typename T, typename TO, int DP, int KT, int OCC, int NW>
 static void launch_many(Attn8Dev d, const Attn8Args& a, hipStream_t st) {
     constexpr int ROWS = 32 * NW;
@@ -969,6 +977,8 @@ hipError_t launch_paged_attn_q8(const Attn8Args& a, hipStream_t st) {
              d.scale_token_stride < k31 && d.scale_token_stride * d.page_size < k31;
     d.page_bytes = (uint32_t)d.page_stride; d.slot_bytes = (uint32_t)d.token_stride;
     d.scale_page = (uint32_t)d.scale_page_stride; d.scale_slot = (uint32_t)d.scale_token_stride;
+    // (by the most queries of the call: single tokens beside a chunk go with the chunk, 63 over up
+    // to 8192 keys beside 512 queries over 2000, 32 heads on 8 of 128, 1469 us, 246 in two calls)
     const bool few = (int64_t)a.max_q * d.G <= 32;
     with_type16(a.q_type, [&](auto t) {
         with_type(a.out_type, [&](auto to) {

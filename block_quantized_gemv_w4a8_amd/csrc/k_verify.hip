@@ -18,7 +18,7 @@
 // each chunk; the draw.  Certain drafts leave the chunks' own sums but for one, so the
 // second goes into the third.  (With the draw left to the workgroup that comes last, the
 // releases of memory that this takes made the second launch 31 us of 84.)  48 sequences
-// of up to five rows of 128256 fp32 logits take 48 to 50 us: 29.5, 12.5 and 6.  The first
+// of up to five rows of 128256 fp32 logits take 48 to 51 us: 29.5, 12.5 and 6.  The first
 // is bound by the vector pipe (0.82 busy, 28 instructions a value of which 17 are the
 // exponential and its sum; the bytes take 3.8 TB/s), the others by the way through stats,
 // logits and sums.

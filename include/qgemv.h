@@ -563,7 +563,9 @@ qgemv_status qgemv_rope_append_q8(const qgemv_kv_cache_q8* cache, int64_t T, int
  * row's largest weight times its largest seen scale).  It is taken as two fp16, which
  * leaves 2^-22 of it, where out is fp32, and for fp16 where max_q times the heads of a
  * group is at most 32.  What scales below 2^-60 contribute may be lost, and rows that see
- * one above 2^60 are slow.
+ * one above 2^60 are slow.  Single tokens go through the kernel of few rows only where
+ * max_q times the heads of a group is at most 32: beside chunks they are several times
+ * faster in a call of their own.
  * Argument conventions, limits and errors as for qgemv_paged_attn. */
 qgemv_status qgemv_paged_attn_q8(const qgemv_kv_cache_q8* cache, const void* q, int q_type,
                                  int64_t T, int64_t ldq, int q_heads, const int32_t* q_start,
