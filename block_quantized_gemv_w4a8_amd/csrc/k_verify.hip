@@ -450,7 +450,7 @@ __device__ Choice choose(const VerifyDev& a, int b, const Seq& s) {
     return Choice{at, stop};
 }
 
-// What is accepted, and the sums of what a refused draft leaves of each chunk, PER a wave.
+// What is accepted, and the sums of what a refused draft leaves of each chunk, PER chunks a wave.
 template <typename T, int PER>
 __global__ __launch_bounds__(VWG) void k_verify_left(const VerifyDev a) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.y;
